@@ -65,12 +65,13 @@ typedef enum {
     DCP_DECODE_MERGED = 1,   /* the merged output: dcp_decode_merged */
     DCP_DECODE_RANK = 2      /* one rank's shard of a multi-GPU group: dcp_decode_rank */
 } dcp_decode_mode;
-typedef enum { DCP_BF16 = 0, DCP_FP8_E4M3 = 1 } dcp_dtype;
+typedef enum { DCP_BF16 = 0, DCP_FP8_E4M3 = 1, DCP_FP4_E2M1 = 2 } dcp_dtype;
 
 /*
  * The sharded paged KV cache.
  *
- *  kind/dtype   DCP_GQA with DCP_BF16; or DCP_MLA with DCP_BF16 or DCP_FP8_E4M3.
+ *  kind/dtype   DCP_GQA with DCP_BF16 or DCP_FP4_E2M1; or DCP_MLA with DCP_BF16 or
+ *               DCP_FP8_E4M3.
  *  n_shards     N >= 1: shards of the sequence dimension.
  *  interleave   I >= 1: position p belongs to shard (p / I) mod N; within a
  *               shard the owned positions are packed in increasing order, so
@@ -83,11 +84,21 @@ typedef enum { DCP_BF16 = 0, DCP_FP8_E4M3 = 1 } dcp_dtype;
  *               576 (512 + 64 rope), dv = 512; the value is the first dv
  *               entries of the latent row (absorbed MLA).
  *  scale        softmax scale applied to q.k.
- *  k_pages      GQA: keys   [num_pages][hkv][P][dk] bf16.
+ *  k_pages      GQA: keys   [num_pages][hkv][P][dk] bf16, or for fp4
+ *               [num_pages][hkv] blocks of P * (dk/2 + dk/16) bytes (below).
  *               MLA: latent [num_pages][P][576] bf16, or e4m3 bytes for fp8.
- *  v_pages      GQA: values [num_pages][hkv][P][dv] bf16.  MLA: NULL.
+ *  v_pages      GQA: values, laid out as k_pages.  MLA: NULL.
  *  kv_scales    MLA fp8: per-token fp32 scale [num_pages][P]; value of latent
- *               element = e4m3(code) * scale.  Otherwise NULL.
+ *               element = e4m3(code) * scale.  GQA fp4: fp32 [2], the factors
+ *               of all keys and of all values (finite, > 0), or NULL for 1 and
+ *               1.  Otherwise NULL.
+ *
+ *  A 4-bit block holds one KV head's rows of one page: P rows of dk/2 bytes
+ *  of e2m1 codes (dimension 2i in the low half of byte i, 2i + 1 in the high
+ *  half), then dk/16 rows of P bytes of e4m3 scales (byte t of row j: token
+ *  t, dimensions 16j .. 16j+15).  Value = e2m1(code) * e4m3(scale) * factor:
+ *  4.5 bits for each.
+ *
  *  block_tables int32 [n_shards][batch][max_local_pages]: shard n's local page
  *               j of request b is pool page block_tables[n][b][j]; -1 = none.
  *  batch        B: requests (rows of each shard's block table).
@@ -157,13 +168,114 @@ dcp_status dcp_shard_map(const dcp_cache_desc* cache, int64_t n_pos, const int32
  *  k_new      GQA: bf16 [n_tok][hkv][dk].  MLA: latent bf16 [n_tok][576]; for an
  *             fp8 cache the row is quantised on the way in: scale = amax/448
  *             (fp32), code = round-to-nearest-even(x / scale) saturated to
- *             +-448; amax = 0 stores scale 1 and zero codes.
+ *             +-448; amax = 0 stores scale 1 and zero codes.  For a 4-bit cache
+ *             each run of 16 dimensions gets scale = e4m3(amax / (6 factor)),
+ *             rounded to nearest even and saturated at 448, and code =
+ *             e2m1(x / (scale factor)), rounded to nearest even and saturated
+ *             at +-6; a scale that rounds to 0 stores zero codes, and a run
+ *             with a NaN stores the NaN scale, so that all of it reads as NaN.
  *  v_new      GQA: bf16 [n_tok][hkv][dv].  MLA: NULL.
  * Rows whose slot is unallocated are skipped and the device status word
  * records DCP_ERR_UNALLOCATED_PAGE.  Two rows with the same (req, pos) race.
  */
 dcp_status dcp_kv_append(const dcp_cache_desc* cache, int64_t n_tok, const int32_t* req, const int32_t* pos,
                          const void* k_new, const void* v_new, void* stream);
+
+/*
+ * dcp_kv_gather -- read tokens' rows back from the pages of the shards that own
+ * them, as bf16: the inverse of dcp_kv_append, for code that needs the values a
+ * quantised cache stands for, or the rows in another order.
+ *  rank       -1: the cache holds every shard; r: the cache of rank r of a group
+ *             (rows that other ranks own are left as they were).
+ *  n_tok, req, pos   as dcp_kv_append; a position may be listed more than once.
+ *  k_out      GQA: bf16 [n_tok][hkv][dk].  MLA: bf16 [n_tok][576].
+ *  v_out      GQA: bf16 [n_tok][hkv][dv], or NULL.  MLA: NULL.
+ * A bf16 row comes back bit for bit and a 4-bit row exactly (code times scale has
+ * 6 significant bits) unless its cache has factors; what an fp8 or a factor
+ * product has beyond 8 bits is rounded to nearest even, once.  A row whose slot is unallocated is left as
+ * it was and the device status word records DCP_ERR_UNALLOCATED_PAGE.
+ * Errors: DCP_ERR_INVALID_ARG, DCP_ERR_MISALIGNED, DCP_ERR_UNSUPPORTED as
+ * dcp_kv_append; rank outside [-1, n_shards) is DCP_ERR_INVALID_ARG.
+ */
+dcp_status dcp_kv_gather(const dcp_cache_desc* cache, int32_t rank, int64_t n_tok, const int32_t* req,
+                         const int32_t* pos, void* k_out, void* v_out, void* stream);
+
+/* How the two members of a rotated pair lie in a row of rot_dim dimensions: i and
+ * i + rot_dim/2, or 2i and 2i + 1. */
+typedef enum { DCP_ROPE_HALF = 0, DCP_ROPE_INTERLEAVED = 1 } dcp_rope_layout;
+
+/* How the frequencies theta^(-2i/rot_dim) are changed for contexts longer than the
+ * model was trained on (dcp_rope_init). */
+typedef enum {
+    DCP_ROPE_NONE = 0,
+    DCP_ROPE_LINEAR = 1,  /* every frequency / factor */
+    DCP_ROPE_BASE = 2,    /* theta * factor^(rot_dim / (rot_dim - 2)) in theta's place */
+    DCP_ROPE_YARN = 3,    /* / factor for pairs that turn fewer than `low` times within `original` positions,
+                             unchanged above `high` turns, a ramp over the pair's index between */
+    DCP_ROPE_SMOOTH = 4   /* the same ends, interpolated by the number of turns itself */
+} dcp_rope_scaling;
+
+#define DCP_ROPE_MAX_PAIRS 64
+
+/*
+ * A position rotation, HOST memory, filled by dcp_rope_init.  turns[i] is pair i's
+ * frequency in units of 2^-64 turns for each position, so that position times
+ * turns[i] modulo 2^64 is the angle modulo a whole turn without a rounding: far
+ * positions keep every bit that cosine and sine need.
+ */
+typedef struct {
+    int32_t rot_dim;      /* rotated dimensions, a multiple of 16 */
+    int32_t layout;       /* dcp_rope_layout */
+    float attn_factor;    /* multiplies cosine and sine */
+    int32_t reserved0;
+    uint64_t turns[DCP_ROPE_MAX_PAIRS];
+} dcp_rope;
+
+/*
+ * dcp_rope_init -- fill *rope (host function; no GPU work).
+ *  rot_dim    16, 32, ... 128.
+ *  theta      base of the frequencies, finite and > 1.
+ *  scaling    dcp_rope_scaling; factor (finite, >= 1), original (> 0), low and high
+ *             (0 < low < high) are read only by the kinds that use them.
+ *  attn_factor  0: 1, and for DCP_ROPE_YARN 0.1 ln(factor) + 1; otherwise the
+ *             factor itself (finite, > 0).
+ * Errors: DCP_ERR_INVALID_ARG, DCP_ERR_UNSUPPORTED (rot_dim).
+ */
+dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                         double factor, double original, double low, double high, double attn_factor);
+
+/*
+ * dcp_norm_rope_append -- norms of queries and keys for each head, the rotation of
+ * their positions and dcp_kv_append, in one pass over the projections' output.
+ *  rank       -1: the cache holds every shard; r: the cache of rank r of a group,
+ *             which stores the rows it owns (q_out is written for every token).
+ *  rope       HOST; GQA: rot_dim <= dk, the first rot_dim dimensions of each head
+ *             are rotated.  MLA: rot_dim = 64, the last 64 of the 576.  NULL: no
+ *             rotation.
+ *  n_tok, req, pos   as dcp_kv_append.  pos < 0 marks a padding token: its row of
+ *             q_out and the cache are left as they were, without an error.
+ *  q          bf16, token i's hq rows of dk at q + i * q_stride (elements); NULL:
+ *             keys and values only.
+ *  k          GQA: bf16, token i's hkv rows of dk at k + i * k_stride.  MLA: its
+ *             latent row of 576.  NULL: queries only (nothing is appended).
+ *  v          GQA: as k, appended as it is.  MLA: NULL.
+ *  q_weight   bf16 [dk], or NULL: q's rows are not normed.  MLA: NULL.
+ *  k_weight   bf16 [dk] (MLA: [512], over the first 512 of the latent row), or
+ *             NULL: k's rows are not normed.
+ *  eps        >= 0: y = x / sqrt(mean x^2 + eps) * weight.
+ *  q_out      bf16 [n_tok][hq][dk], NULL only without q.  May be q itself when
+ *             q_stride = hq * dk (MLA then touches the rotated part only).
+ * Norm and rotation are computed in 32 bits and rounded to bf16 once; a quantised
+ * cache then stores that row as dcp_kv_append would.  Strides are multiples of 8
+ * elements.  Two tokens with the same (req, pos) race, as in dcp_kv_append.  Rows
+ * whose slot is unallocated are skipped and the device status word records
+ * DCP_ERR_UNALLOCATED_PAGE (their q_out rows are written).
+ * Errors: DCP_ERR_INVALID_ARG, DCP_ERR_MISALIGNED, DCP_ERR_UNSUPPORTED.
+ */
+dcp_status dcp_norm_rope_append(const dcp_cache_desc* cache, int32_t rank, const dcp_rope* rope, int64_t n_tok,
+                                const int32_t* req, const int32_t* pos, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const void* q_weight, const void* k_weight, float eps, void* q_out, void* stream);
 
 /*
  * dcp_decode_workspace_size -- bytes of device workspace dcp_decode_partial
@@ -224,8 +336,9 @@ size_t dcp_decode_workspace_size_ex(const dcp_cache_desc* cache, int32_t B, int3
  * new tokens, and query token j attends the positions p <= L_b - q_len + j.
  *  q_len      1 <= q_len <= 64.  q_len > 1 is served by the tensor-core
  *             kernels only: MLA with 64-token pages and q_len * hq in
- *             {16, 32, 64}; GQA with q_len * hq / hkv == 16.  Other shapes
- *             return DCP_ERR_UNSUPPORTED.
+ *             {16, 32, 64}; bf16 GQA with q_len * hq / hkv == 16; GQA over a
+ *             4-bit cache with any group size.  Other shapes return
+ *             DCP_ERR_UNSUPPORTED.
  *  q          bf16 [B][q_len][hq][dk].
  *  seq_lens   int32 [B]: L_b, which must be 0 or >= q_len (0 < L_b < q_len
  *             records DCP_ERR_INVALID_ARG in the device status word; such a
@@ -273,6 +386,36 @@ dcp_status dcp_decode_partial_multi(const dcp_cache_desc* cache, int32_t B, int3
 dcp_status dcp_decode_merged(const dcp_cache_desc* cache, int32_t B, int32_t q_len, const void* q,
                              const int32_t* seq_lens, float* out, float* lse_out, int64_t* finish_ns, void* ws,
                              size_t ws_bytes, void* stream);
+
+/*
+ * dcp_decode_window -- decode attention that sees a sliding window and a few first
+ * tokens: query token j of request b stands at i = L_b - q_len + j and attends the
+ * positions p <= i with p < n_sinks or p > i - window.  GQA caches, bf16 or 4-bit,
+ * any group size.
+ *  rank       -1: every shard, merged (the output of dcp_decode_merged under this
+ *             mask).  r: the cache of rank r of a group; out and lse are its
+ *             partial, as dcp_decode_rank's, to be exchanged in the same way.
+ *  window     >= 1: positions a query token sees, itself among them.
+ *  n_sinks    >= 0: first positions that stay visible.
+ *  q_len, q, seq_lens   as dcp_decode_partial_multi.
+ *  out        fp32 [B][q_len][hq][dv], 0 where a query token attends no position.
+ *  lse        fp32 [B][q_len][hq], natural log, -inf where it attends none.
+ *  ws, ws_bytes   at least dcp_decode_window_workspace_size() bytes of the same
+ *             arguments; clobbered.  Concurrent calls need distinct workspaces.
+ * Pages behind the window are not read: their block-table entries may be -1 or
+ * reused.  Keys and values that no query token attends may hold anything.
+ * Errors as dcp_decode_partial; DCP_ERR_UNSUPPORTED for MLA caches.
+ */
+dcp_status dcp_decode_window(const dcp_cache_desc* cache, int32_t rank, int32_t B, int32_t q_len, int32_t window,
+                             int32_t n_sinks, const void* q, const int32_t* seq_lens, float* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * dcp_decode_window_workspace_size -- bytes dcp_decode_window needs on the CURRENT
+ * device (host function; no GPU work).  0 for arguments that the call refuses.
+ */
+size_t dcp_decode_window_workspace_size(const dcp_cache_desc* cache, int32_t rank, int32_t B, int32_t q_len,
+                                        int32_t window, int32_t n_sinks);
 
 /*
  * Several GPUs: the cache of ONE rank of an N-GPU group.

@@ -11,8 +11,9 @@ Entry points (same names as ``include/dcp.h``): ``dcp_shard_counts``,
 ``dcp_shard_map``, ``dcp_kv_append``, ``dcp_decode_workspace_size``,
 ``dcp_decode_workspace_size_ex``, ``dcp_decode_partial``,
 ``dcp_decode_partial_multi``, ``dcp_decode_merged``,
-``dcp_decode_partial_noalloc``, ``dcp_merge``, ``dcp_get_device_status``, and for
-one rank of a multi-GPU group ``dcp_kv_append_rank``, ``dcp_decode_rank``,
+``dcp_decode_partial_noalloc``, ``dcp_merge``, ``dcp_get_device_status``,
+``dcp_norm_rope_append`` (with ``make_rope``), ``dcp_kv_gather``,
+``dcp_decode_window``, and for one rank of a multi-GPU group ``dcp_kv_append_rank``, ``dcp_decode_rank``,
 ``dcp_lse_rescale`` (the collectives around them are in ``parallel.py``).
 """
 from __future__ import annotations
@@ -36,6 +37,11 @@ DCP_GQA = 0
 DCP_MLA = 1
 DCP_BF16 = 0
 DCP_FP8_E4M3 = 1
+DCP_FP4_E2M1 = 2
+
+DCP_ROPE_HALF = 0
+DCP_ROPE_INTERLEAVED = 1
+ROPE_SCALINGS = ("none", "linear", "base", "yarn", "smooth")  # dcp_rope_scaling, in order
 
 DCP_DECODE_PARTIAL = 0
 DCP_DECODE_MERGED = 1
@@ -44,7 +50,8 @@ DCP_DECODE_RANK = 2
 EXPORTED = ("dcp_status_string", "dcp_shard_counts", "dcp_shard_map", "dcp_kv_append",
             "dcp_decode_workspace_size", "dcp_decode_workspace_size_ex", "dcp_decode_partial",
             "dcp_decode_partial_multi", "dcp_decode_merged", "dcp_decode_partial_noalloc", "dcp_merge",
-            "dcp_get_device_status", "dcp_kv_append_rank", "dcp_decode_rank", "dcp_lse_rescale")
+            "dcp_get_device_status", "dcp_kv_append_rank", "dcp_decode_rank", "dcp_lse_rescale", "dcp_kv_gather",
+            "dcp_rope_init", "dcp_norm_rope_append", "dcp_decode_window", "dcp_decode_window_workspace_size")
 
 
 class DcpError(RuntimeError):
@@ -65,6 +72,12 @@ class CacheDesc(ctypes.Structure):
         ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
         ("kv_scales", ctypes.c_void_p), ("block_tables", ctypes.c_void_p),
     ]
+
+
+class Rope(ctypes.Structure):
+    """Mirror of ``dcp_rope`` (host memory; filled by :func:`dcp_rope_init`)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("attn_factor", ctypes.c_float),
+                ("reserved0", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
 
 
 _lib = None
@@ -94,6 +107,14 @@ def lib() -> ctypes.CDLL:
         L.dcp_kv_append_rank.argtypes = [D, i32, i64, P, P, P, P, P]
         L.dcp_decode_rank.argtypes = [D, i32, i32, i32, P, P, P, P, P, ctypes.c_size_t, P]
         L.dcp_lse_rescale.argtypes = [i32, i32, i32, i32, i32, P, P, P, P, P]
+        F64 = ctypes.c_double
+        R = ctypes.POINTER(Rope)
+        L.dcp_kv_gather.argtypes = [D, i32, i64, P, P, P, P, P]
+        L.dcp_rope_init.argtypes = [R, i32, i32, F64, i32, F64, F64, F64, F64, F64]
+        L.dcp_norm_rope_append.argtypes = [D, i32, R, i64, P, P, P, i64, P, i64, P, i64, P, P, ctypes.c_float, P, P]
+        L.dcp_decode_window.argtypes = [D, i32, i32, i32, i32, i32, P, P, P, P, P, ctypes.c_size_t, P]
+        L.dcp_decode_window_workspace_size.argtypes = [D, i32, i32, i32, i32, i32]
+        L.dcp_decode_window_workspace_size.restype = ctypes.c_size_t
         L.dcp_decode_partial_noalloc.argtypes = [D, i32, P, P, P, P, P]
         L.dcp_merge.argtypes = [i32, i32, i32, i32, P, P, P, P, P]
         L.dcp_get_device_status.argtypes = [ctypes.POINTER(i32), P]
@@ -101,7 +122,8 @@ def lib() -> ctypes.CDLL:
         for name in ("dcp_shard_counts", "dcp_shard_map", "dcp_kv_append", "dcp_decode_partial",
                      "dcp_decode_partial_multi", "dcp_decode_merged", "dcp_decode_partial_noalloc", "dcp_merge",
                      "dcp_get_device_status", "dcp_kv_append_rank", "dcp_decode_rank", "dcp_lse_rescale",
-                     "dcp_selftest_bounded_wait"):
+                     "dcp_selftest_bounded_wait", "dcp_kv_gather", "dcp_rope_init", "dcp_norm_rope_append",
+                     "dcp_decode_window"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -204,6 +226,125 @@ def dcp_lse_rescale(lse_all, rank: int, o, o_rs, lse_out=None, stream=None) -> N
     N, B, H = lse_all.shape
     _check(lib().dcp_lse_rescale(N, rank, B, H, o.shape[-1], _ptr(lse_all), _ptr(o), _ptr(o_rs), _ptr(lse_out),
                                  _stream(stream)), "dcp_lse_rescale")
+
+
+def _tensor(name: str, t, dtype: str, shape=None) -> None:
+    """Refuse a tensor whose layout the kernels would misread (torch tensors on the current device)."""
+    import torch
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if t.dtype is not getattr(torch, dtype):
+        raise ValueError(f"{name} is {t.dtype}, not torch.{dtype}")
+    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+        raise ValueError(f"{name} is {tuple(t.shape)} (strides {t.stride()}), not a contiguous {tuple(shape)}")
+
+
+def _rank(rank) -> int:
+    return -1 if rank is None else int(rank)
+
+
+def _tokens(desc: CacheDesc, req, pos) -> int:
+    n = pos.numel()
+    _tensor("pos", pos, "int32", (n,))
+    if req is not None:
+        _tensor("req", req, "int32", (n,))
+    elif n > desc.batch:
+        raise ValueError(f"{n} tokens without req: row i belongs to request i of {desc.batch}")
+    return n
+
+
+def dcp_kv_gather(desc: CacheDesc, req, pos, k_out, v_out=None, rank=None, stream=None) -> None:
+    """Read rows back as bf16: k_out [n][hkv][dk] (MLA [n][576]), v_out alike or None."""
+    n = _tokens(desc, req, pos)
+    shape = (n, desc.hkv, desc.dk) if desc.kind == DCP_GQA else (n, desc.dk)
+    _tensor("k_out", k_out, "bfloat16", shape)
+    if v_out is not None:
+        _tensor("v_out", v_out, "bfloat16", shape)
+    _check(lib().dcp_kv_gather(ctypes.byref(desc), _rank(rank), n, _ptr(req), _ptr(pos), _ptr(k_out), _ptr(v_out),
+                               _stream(stream)), "dcp_kv_gather")
+
+
+def dcp_rope_init(rope: Rope, rot_dim: int, layout: int, theta: float, scaling: int = 0, factor: float = 1.0,
+                  original: float = 0.0, low: float = 0.0, high: float = 0.0, attn_factor: float = 0.0) -> None:
+    _check(lib().dcp_rope_init(ctypes.byref(rope), rot_dim, layout, theta, scaling, factor, original, low, high,
+                               attn_factor), "dcp_rope_init")
+
+
+def make_rope(rot_dim: int, *, layout: str = "half", theta: float = 1e4, scaling: str = "none", factor: float = 1.0,
+              original: float = 0.0, low: float = 1.0, high: float = 32.0, attn_factor: float = 0.0) -> Rope:
+    """A position rotation for dcp_norm_rope_append: layout "half" or "interleaved", scaling one of
+    ``ROPE_SCALINGS`` (include/dcp.h says what each does with factor, original, low and high)."""
+    layouts = {"half": DCP_ROPE_HALF, "interleaved": DCP_ROPE_INTERLEAVED}
+    if layout not in layouts or scaling not in ROPE_SCALINGS:
+        raise ValueError(f"unknown rotary layout {layout!r} or scaling {scaling!r}")
+    rope = Rope()
+    dcp_rope_init(rope, rot_dim, layouts[layout], theta, ROPE_SCALINGS.index(scaling), factor, original, low, high,
+                  attn_factor)
+    return rope
+
+
+def _rows(name: str, t, shape) -> int:
+    """Token stride (elements) of rows [n][..] whose inner dimensions are contiguous."""
+    _tensor(name, t, "bfloat16")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size > 1 and stride != inner:
+            raise ValueError(f"{name}: a token's row is not contiguous (strides {t.stride()})")
+        inner *= size
+    return t.stride(0) if t.shape[0] > 1 else inner
+
+
+def dcp_norm_rope_append(desc: CacheDesc, rope, req, pos, q, k, v, q_weight, k_weight, eps: float, q_out, rank=None,
+                         stream=None) -> None:
+    """Per-head norms, position rotation and append in one pass.
+
+    q bf16 [n][hq][dk], k / v bf16 [n][hkv][dk] (MLA: k [n][576], v None), rows may be strided by token (slices of
+    one projection's output); q_weight / k_weight bf16 [dk] (MLA: None and [512]) or None for no norm; rope from
+    make_rope or None; q_out bf16 [n][hq][dk], which may be q itself.  q and q_out, or k and v, may be None."""
+    n = _tokens(desc, req, pos)
+    mla = desc.kind == DCP_MLA
+    qs = ks = vs = 0
+    if q is not None:
+        qs = _rows("q", q, (n, desc.hq, desc.dk))
+        if q_out is None:
+            raise ValueError("q without q_out")
+        _tensor("q_out", q_out, "bfloat16", (n, desc.hq, desc.dk))
+    kv_shape = (n, desc.dk) if mla else (n, desc.hkv, desc.dk)
+    if k is not None:
+        ks = _rows("k", k, kv_shape)
+    if v is not None:
+        vs = _rows("v", v, kv_shape)
+    if q_weight is not None:
+        _tensor("q_weight", q_weight, "bfloat16", (desc.dk,))
+    if k_weight is not None:
+        _tensor("k_weight", k_weight, "bfloat16", (512 if mla else desc.dk,))
+    _check(lib().dcp_norm_rope_append(ctypes.byref(desc), _rank(rank), None if rope is None else ctypes.byref(rope), n,
+                                      _ptr(req), _ptr(pos), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
+                                      _ptr(k_weight), eps, _ptr(q_out if q is not None else None), _stream(stream)),
+           "dcp_norm_rope_append")
+
+
+def dcp_decode_window_workspace_size(desc: CacheDesc, batch: int, q_len: int, window: int, n_sinks: int = 0,
+                                     rank=None) -> int:
+    return int(lib().dcp_decode_window_workspace_size(ctypes.byref(desc), _rank(rank), batch, q_len, window, n_sinks))
+
+
+def dcp_decode_window(desc: CacheDesc, q, seq_lens, window: int, n_sinks: int, out, lse, ws, rank=None,
+                      stream=None) -> None:
+    """Decode attention under a sliding window of `window` positions and `n_sinks` first tokens.
+    q bf16 [B][hq][dk] or [B][q_len][hq][dk]; out / lse fp32 with q's leading dimensions; rank None: all shards
+    merged, r: rank r's partial of a multi-GPU group."""
+    lead = tuple(q.shape[:-1])
+    q_len = 1 if q.dim() == 3 else q.shape[1]
+    _tensor("q", q, "bfloat16", lead[:-1] + (desc.hq, desc.dk))
+    _tensor("seq_lens", seq_lens, "int32", (q.shape[0],))
+    _tensor("out", out, "float32", lead + (desc.dv,))
+    _tensor("lse", lse, "float32", lead)
+    _check(lib().dcp_decode_window(ctypes.byref(desc), _rank(rank), q.shape[0], q_len, window, n_sinks, _ptr(q),
+                                   _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _stream(stream)), "dcp_decode_window")
 
 
 # size of the library's built-in decode scratch (DCP_STATIC_SCRATCH_BYTES in dcp.h)

@@ -1,6 +1,9 @@
 // api.cu -- the C ABI of libdcp (include/dcp.h): host-side validation, the
 // sticky device status word, workspace sizing and kernel dispatch.
 #include <cudaTypedefs.h>
+#include <limits.h>
+
+#include <cmath>
 
 #include <mutex>
 
@@ -112,13 +115,16 @@ dcp_status check_desc(const dcp_cache_desc* c, bool need_pools) {
     if (!c->block_tables) return DCP_ERR_INVALID_ARG;
     if (c->hq < 1 || c->hkv < 1 || c->hq % c->hkv) return DCP_ERR_INVALID_ARG;
     if (c->kind == DCP_GQA) {
-        if (c->dtype != DCP_BF16) return DCP_ERR_UNSUPPORTED;
+        if (c->dtype != DCP_BF16 && c->dtype != DCP_FP4_E2M1) return DCP_ERR_UNSUPPORTED;
         if (c->dk != c->dv || (c->dk != 64 && c->dk != 128)) return DCP_ERR_UNSUPPORTED;
         if (need_pools && (!c->k_pages || !c->v_pages)) return DCP_ERR_INVALID_ARG;
         if (need_pools && (!aligned16(c->k_pages) || !aligned16(c->v_pages))) return DCP_ERR_MISALIGNED;
+        if (need_pools && c->dtype == DCP_FP4_E2M1 && c->kv_scales && !aligned16(c->kv_scales))
+            return DCP_ERR_MISALIGNED;
     } else if (c->kind == DCP_MLA) {
         if (c->hkv != 1 || c->dk != 576 || c->dv != 512) return DCP_ERR_UNSUPPORTED;
         if (c->hq % 16) return DCP_ERR_UNSUPPORTED;
+        if (c->dtype == DCP_FP4_E2M1) return DCP_ERR_UNSUPPORTED;
         if (c->dtype != DCP_BF16 && c->dtype != DCP_FP8_E4M3) return DCP_ERR_INVALID_ARG;
         if (need_pools && !c->k_pages) return DCP_ERR_INVALID_ARG;
         if (need_pools && c->dtype == DCP_FP8_E4M3 && !c->kv_scales) return DCP_ERR_INVALID_ARG;
@@ -146,6 +152,26 @@ struct Plan {
 };
 
 constexpr int kMaxQueryLen = 64;
+
+// 4-bit caches are decoded by the warp-streamed kernel, which plans in the kernel
+// and merges the shards itself: its workspace is laid out by StreamPlan.
+bool streamed(const dcp_cache_desc* c) { return c->dtype == DCP_FP4_E2M1; }
+
+bool make_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int mode, int num_sms,
+                      StreamPlan* p) {
+    if (q_len < 1 || q_len > kMaxQueryLen || mode < kModePartial || mode > kModeRank) return false;
+    if (!gqa_stream_supported(c->hq, c->hkv, c->dk, q_len)) return false;
+    *p = gqa_stream_plan(c, q_len, window, sinks, mode == kModeRank ? 1 : c->n_shards, mode == kModePartial, num_sms);
+    return true;
+}
+
+dcp_status stream_on(const dcp_cache_desc* c, const StreamPlan& p, int q_len, int window, int sinks, int mode,
+                     int rank, const void* q, const int32_t* seq_lens, float* out, float* lse, int64_t* finish_ns,
+                     void* ws, int* status, cudaStream_t s) {
+    const int lo = mode == kModeRank ? rank : 0, hi = mode == kModeRank ? rank + 1 : c->n_shards;
+    return cuda_err(launch_gqa_stream(c, p, q_len, window, sinks, lo, hi, mode == kModePartial, lo, q, seq_lens, out,
+                                      lse, finish_ns, ws, status, s));
+}
 
 // The fp8 MLA kernel reads the query split into two e4m3 terms from the end of
 // the workspace: [B][128 rows][576] bytes + [B][64] fp32 reciprocals.
@@ -388,17 +414,9 @@ dcp_status dcp_shard_map(const dcp_cache_desc* cache, int64_t n_pos, const int32
                                      rank_out, local_out, slot_out, status, (cudaStream_t)stream));
 }
 
-static dcp_status kv_append(const dcp_cache_desc* cache, int32_t only_shard, int64_t n_tok, const int32_t* req,
-                            const int32_t* pos, const void* k_new, const void* v_new, void* stream) {
-    dcp_status st = check_desc(cache, true);
-    if (st != DCP_OK) return st;
-    if (n_tok < 0) return DCP_ERR_INVALID_ARG;
-    if (n_tok == 0) return DCP_OK;
-    if (!pos || !k_new || (cache->kind == DCP_GQA && !v_new)) return DCP_ERR_INVALID_ARG;
-    if (!aligned16(k_new) || (v_new && !aligned16(v_new))) return DCP_ERR_MISALIGNED;
-    int* status = nullptr;
-    st = device_info(&status, nullptr);
-    if (st != DCP_OK) return st;
+// Arguments of the kernels that write or read tokens' rows.
+static AppendArgs row_args(const dcp_cache_desc* cache, int32_t only_shard, int64_t n_tok, const int32_t* req,
+                           const int32_t* pos, const void* k_new, const void* v_new, int* status) {
     AppendArgs a;
     a.kind = cache->kind;
     a.dtype = cache->dtype;
@@ -418,11 +436,26 @@ static dcp_status kv_append(const dcp_cache_desc* cache, int32_t only_shard, int
     a.v_new = static_cast<const uint8_t*>(v_new);
     a.k_pages = static_cast<uint8_t*>(cache->k_pages);
     a.v_pages = static_cast<uint8_t*>(cache->v_pages);
-    a.kv_scales = cache->kv_scales;
+    a.kv_scales = cache->kind == DCP_MLA || cache->dtype == DCP_FP4_E2M1 ? cache->kv_scales : nullptr;
     a.block_tables = cache->block_tables;
     a.status = status;
     a.only_shard = only_shard;
-    return cuda_err(launch_append(a, (cudaStream_t)stream));
+    return a;
+}
+
+static dcp_status kv_append(const dcp_cache_desc* cache, int32_t only_shard, int64_t n_tok, const int32_t* req,
+                            const int32_t* pos, const void* k_new, const void* v_new, void* stream) {
+    dcp_status st = check_desc(cache, true);
+    if (st != DCP_OK) return st;
+    if (n_tok < 0) return DCP_ERR_INVALID_ARG;
+    if (n_tok == 0) return DCP_OK;
+    if (!pos || !k_new || (cache->kind == DCP_GQA && !v_new)) return DCP_ERR_INVALID_ARG;
+    if (!aligned16(k_new) || (v_new && !aligned16(v_new))) return DCP_ERR_MISALIGNED;
+    int* status = nullptr;
+    st = device_info(&status, nullptr);
+    if (st != DCP_OK) return st;
+    return cuda_err(launch_append(row_args(cache, only_shard, n_tok, req, pos, k_new, v_new, status),
+                                  (cudaStream_t)stream));
 }
 
 dcp_status dcp_kv_append(const dcp_cache_desc* cache, int64_t n_tok, const int32_t* req, const int32_t* pos,
@@ -436,19 +469,154 @@ dcp_status dcp_kv_append_rank(const dcp_cache_desc* cache, int32_t rank, int64_t
     return kv_append(cache, rank, n_tok, req, pos, k_new, v_new, stream);
 }
 
-size_t dcp_decode_workspace_size(const dcp_cache_desc* cache, int32_t B) {
-    if (check_desc(cache, false) != DCP_OK || B != cache->batch) return 0;
+dcp_status dcp_kv_gather(const dcp_cache_desc* cache, int32_t rank, int64_t n_tok, const int32_t* req,
+                         const int32_t* pos, void* k_out, void* v_out, void* stream) {
+    dcp_status st = check_desc(cache, true);
+    if (st != DCP_OK) return st;
+    if (rank < -1 || rank >= cache->n_shards || n_tok < 0) return DCP_ERR_INVALID_ARG;
+    if (cache->kind == DCP_MLA && v_out) return DCP_ERR_INVALID_ARG;
+    if (n_tok == 0) return DCP_OK;
+    if (!pos || !k_out) return DCP_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || (v_out && !aligned16(v_out))) return DCP_ERR_MISALIGNED;
+    int* status = nullptr;
+    st = device_info(&status, nullptr);
+    if (st != DCP_OK) return st;
+    return cuda_err(launch_gather(row_args(cache, rank, n_tok, req, pos, nullptr, nullptr, status), k_out, v_out,
+                                  (cudaStream_t)stream));
+}
+
+dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,
+                         double factor, double original, double low, double high, double attn_factor) {
+    if (!rope || (layout != DCP_ROPE_HALF && layout != DCP_ROPE_INTERLEAVED)) return DCP_ERR_INVALID_ARG;
+    if (rot_dim < 1 || !(theta > 1.0) || !std::isfinite(theta)) return DCP_ERR_INVALID_ARG;
+    if (scaling < DCP_ROPE_NONE || scaling > DCP_ROPE_SMOOTH) return DCP_ERR_INVALID_ARG;
+    if (scaling != DCP_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return DCP_ERR_INVALID_ARG;
+    const bool ends = scaling == DCP_ROPE_YARN || scaling == DCP_ROPE_SMOOTH;
+    if (ends && (!(original > 0.0) || !std::isfinite(original) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
+        return DCP_ERR_INVALID_ARG;
+    if (!(attn_factor >= 0.0) || !std::isfinite(attn_factor)) return DCP_ERR_INVALID_ARG;
+    if (rot_dim % 16 || rot_dim > 2 * DCP_ROPE_MAX_PAIRS) return DCP_ERR_UNSUPPORTED;
+    const long double two_pi = 6.283185307179586476925286766559005768L;
+    const long double d = rot_dim, f = factor;
+    long double base = theta;
+    if (scaling == DCP_ROPE_BASE) base *= powl(f, d / (d - 2));
+    // index (not whole) of the pair that turns `n` times within `original` positions
+    auto index_of = [&](long double n) { return d * logl(original / (n * two_pi)) / (2 * logl(base)); };
+    *rope = dcp_rope{};
+    rope->rot_dim = rot_dim;
+    rope->layout = layout;
+    rope->attn_factor = attn_factor > 0.0 ? (float)attn_factor
+                        : scaling == DCP_ROPE_YARN ? (float)(0.1L * logl(f) + 1.0L) : 1.f;
+    for (int i = 0; i < rot_dim / 2; i++) {
+        long double w = powl(base, -2.0L * i / d);
+        if (scaling == DCP_ROPE_LINEAR) {
+            w /= f;
+        } else if (scaling == DCP_ROPE_YARN) {
+            const long double lo = fmaxl(floorl(index_of(high)), 0.0L), hi = fminl(ceill(index_of(low)), d - 1);
+            const long double r = fminl(fmaxl((i - lo) / fmaxl(hi - lo, 0.001L), 0.0L), 1.0L);
+            w = w / f * r + w * (1.0L - r);
+        } else if (scaling == DCP_ROPE_SMOOTH) {
+            const long double n = original * w / two_pi;
+            const long double k = fminl(fmaxl((n - low) / ((long double)high - low), 0.0L), 1.0L);
+            w = w * k + w / f * (1.0L - k);
+        }
+        rope->turns[i] = (uint64_t)(w / two_pi * 18446744073709551616.0L + 0.5L);  // w <= 1: below 2^62
+    }
+    return DCP_OK;
+}
+
+dcp_status dcp_norm_rope_append(const dcp_cache_desc* cache, int32_t rank, const dcp_rope* rope, int64_t n_tok,
+                                const int32_t* req, const int32_t* pos, const void* q, int64_t q_stride,
+                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                const void* q_weight, const void* k_weight, float eps, void* q_out, void* stream) {
+    dcp_status st = check_desc(cache, k != nullptr);
+    if (st != DCP_OK) return st;
+    if (rank < -1 || rank >= cache->n_shards || n_tok < 0 || !(eps >= 0.f)) return DCP_ERR_INVALID_ARG;
+    const bool mla = cache->kind == DCP_MLA;
+    if (rope) {
+        if (rope->rot_dim < 16 || rope->rot_dim > 2 * DCP_ROPE_MAX_PAIRS ||
+            (rope->layout != DCP_ROPE_HALF && rope->layout != DCP_ROPE_INTERLEAVED))
+            return DCP_ERR_INVALID_ARG;  // not a dcp_rope_init result
+        if (rope->rot_dim % 16 || (mla ? rope->rot_dim != 64 : rope->rot_dim > cache->dk)) return DCP_ERR_UNSUPPORTED;
+    }
+    if (n_tok == 0) return DCP_OK;
+    if (n_tok > INT32_MAX) return DCP_ERR_UNSUPPORTED;
+    if (!pos || (!q && !k) || (q != nullptr) != (q_out != nullptr)) return DCP_ERR_INVALID_ARG;
+    if (mla ? (v || q_weight) : (k != nullptr) != (v != nullptr)) return DCP_ERR_INVALID_ARG;
+    if ((q_weight && !q) || (k_weight && !k)) return DCP_ERR_INVALID_ARG;
+    const int64_t q_row = (int64_t)cache->hq * cache->dk, k_row = (int64_t)cache->hkv * cache->dk;
+    if ((q && q_stride < q_row) || (k && k_stride < k_row) || (v && v_stride < k_row)) return DCP_ERR_INVALID_ARG;
+    if ((q && q_stride % 8) || (k && k_stride % 8) || (v && v_stride % 8)) return DCP_ERR_MISALIGNED;
+    const void* ptrs[] = {q, k, v, q_weight, k_weight, q_out};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return DCP_ERR_MISALIGNED;
+    if (q) {  // q_out is q exactly, or apart from it
+        const uintptr_t a = reinterpret_cast<uintptr_t>(q), z = a + 2 * ((n_tok - 1) * q_stride + q_row);
+        const uintptr_t oa = reinterpret_cast<uintptr_t>(q_out), oz = oa + 2 * n_tok * q_row;
+        if (oa < z && a < oz && !(oa == a && q_stride == q_row)) return DCP_ERR_INVALID_ARG;
+    }
+    int* status = nullptr;
+    int num_sms = 0;
+    st = device_info(&status, &num_sms);
+    if (st != DCP_OK) return st;
+    return cuda_err(launch_norm_rope_append(row_args(cache, rank, n_tok, req, pos, k, v, status), rope, q, q_stride,
+                                            k_stride, v_stride, q_weight, k_weight, eps, q_out, cache->hq, num_sms,
+                                            (cudaStream_t)stream));
+}
+
+// Checks that dcp_decode_window and its workspace size share.
+static dcp_status check_window(const dcp_cache_desc* cache, int32_t rank, int32_t B, int32_t q_len, int32_t window,
+                               int32_t n_sinks, bool need_pools) {
+    dcp_status st = check_desc(cache, need_pools);
+    if (st != DCP_OK) return st;
+    if (rank < -1 || rank >= cache->n_shards || B != cache->batch || q_len < 1 || window < 1 || n_sinks < 0)
+        return DCP_ERR_INVALID_ARG;
+    if (cache->kind != DCP_GQA || q_len > kMaxQueryLen) return DCP_ERR_UNSUPPORTED;
+    return DCP_OK;
+}
+
+size_t dcp_decode_window_workspace_size(const dcp_cache_desc* cache, int32_t rank, int32_t B, int32_t q_len,
+                                        int32_t window, int32_t n_sinks) {
+    if (check_window(cache, rank, B, q_len, window, n_sinks, false) != DCP_OK) return 0;
     int num_sms = 0;
     if (device_info(nullptr, &num_sms) != DCP_OK) return 0;
-    Plan p;
-    if (!make_plan(cache, B, 1, kModePartial, num_sms, &p)) return 0;
-    return p.lay.total;
+    StreamPlan p;
+    if (!make_stream_plan(cache, q_len, window, n_sinks, rank < 0 ? kModeMerged : kModeRank, num_sms, &p)) return 0;
+    return p.total;
+}
+
+dcp_status dcp_decode_window(const dcp_cache_desc* cache, int32_t rank, int32_t B, int32_t q_len, int32_t window,
+                             int32_t n_sinks, const void* q, const int32_t* seq_lens, float* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream) {
+    dcp_status st = check_window(cache, rank, B, q_len, window, n_sinks, true);
+    if (st != DCP_OK) return st;
+    if (!q || !seq_lens || !out || !lse || !ws) return DCP_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(ws)) return DCP_ERR_MISALIGNED;
+    int* status = nullptr;
+    int num_sms = 0;
+    st = device_info(&status, &num_sms);
+    if (st != DCP_OK) return st;
+    const int mode = rank < 0 ? kModeMerged : kModeRank;
+    StreamPlan p;
+    if (!make_stream_plan(cache, q_len, window, n_sinks, mode, num_sms, &p)) return DCP_ERR_UNSUPPORTED;
+    if (ws_bytes < p.total) return DCP_ERR_WORKSPACE_TOO_SMALL;
+    return stream_on(cache, p, q_len, window, n_sinks, mode, rank, q, seq_lens, out, lse, nullptr, ws, status,
+                     (cudaStream_t)stream);
+}
+
+size_t dcp_decode_workspace_size(const dcp_cache_desc* cache, int32_t B) {
+    if (check_desc(cache, false) != DCP_OK || B != cache->batch) return 0;
+    return dcp_decode_workspace_size_ex(cache, B, 1, kModePartial);
 }
 
 size_t dcp_decode_workspace_size_ex(const dcp_cache_desc* cache, int32_t B, int32_t q_len, int32_t mode) {
     if (check_desc(cache, false) != DCP_OK || B != cache->batch) return 0;
     int num_sms = 0;
     if (device_info(nullptr, &num_sms) != DCP_OK) return 0;
+    if (streamed(cache)) {
+        StreamPlan sp;
+        return make_stream_plan(cache, q_len, INT_MAX, 0, mode, num_sms, &sp) ? sp.total : 0;
+    }
     Plan p;
     if (!make_plan(cache, B, q_len, mode, num_sms, &p)) return 0;
     return p.lay.total;
@@ -464,6 +632,13 @@ dcp_status dcp_decode_partial(const dcp_cache_desc* cache, int32_t B, const void
     int num_sms = 0;
     st = device_info(&status, &num_sms);
     if (st != DCP_OK) return st;
+    if (streamed(cache)) {
+        StreamPlan sp;
+        if (!make_stream_plan(cache, 1, INT_MAX, 0, kModePartial, num_sms, &sp)) return DCP_ERR_UNSUPPORTED;
+        if (ws_bytes < sp.total) return DCP_ERR_WORKSPACE_TOO_SMALL;
+        return stream_on(cache, sp, 1, INT_MAX, 0, kModePartial, -1, q, seq_lens, o_partial, lse, nullptr, ws, status,
+                         (cudaStream_t)stream);
+    }
     Plan p;
     if (!make_plan(cache, B, 1, kModePartial, num_sms, &p)) return DCP_ERR_UNSUPPORTED;
     if (ws_bytes < p.lay.total) return DCP_ERR_WORKSPACE_TOO_SMALL;
@@ -486,6 +661,13 @@ static dcp_status decode_ex(const dcp_cache_desc* cache, int32_t B, int32_t q_le
     int num_sms = 0;
     st = device_info(&status, &num_sms);
     if (st != DCP_OK) return st;
+    if (streamed(cache)) {
+        StreamPlan sp;
+        if (!make_stream_plan(cache, q_len, INT_MAX, 0, mode, num_sms, &sp)) return DCP_ERR_UNSUPPORTED;
+        if (ws_bytes < sp.total) return DCP_ERR_WORKSPACE_TOO_SMALL;
+        return stream_on(cache, sp, q_len, INT_MAX, 0, mode, rank, q, seq_lens, out, lse, finish_ns, ws, status,
+                         (cudaStream_t)stream);
+    }
     Plan p;
     if (!make_plan(cache, B, q_len, mode, num_sms, &p)) return DCP_ERR_UNSUPPORTED;
     if (ws_bytes < p.lay.total) return DCP_ERR_WORKSPACE_TOO_SMALL;
@@ -537,6 +719,16 @@ dcp_status dcp_decode_partial_noalloc(const dcp_cache_desc* cache, int32_t B, co
     int num_sms = 0;
     st = device_info(&status, &num_sms);
     if (st != DCP_OK) return st;
+    if (streamed(cache)) {
+        StreamPlan sp;
+        if (!make_stream_plan(cache, 1, INT_MAX, 0, kModePartial, num_sms, &sp)) return DCP_ERR_UNSUPPORTED;
+        if (sp.total > DCP_STATIC_SCRATCH_BYTES) return DCP_ERR_WORKSPACE_TOO_SMALL;
+        uint8_t* w = nullptr;
+        st = decode_scratch(&w);
+        if (st != DCP_OK) return st;
+        return stream_on(cache, sp, 1, INT_MAX, 0, kModePartial, -1, q, seq_lens, o_partial, lse, nullptr, w, status,
+                         (cudaStream_t)stream);
+    }
     Plan p;
     if (!make_plan(cache, B, 1, kModePartial, num_sms, &p)) return DCP_ERR_UNSUPPORTED;
     if (!make_plan_within(cache, B, num_sms, DCP_STATIC_SCRATCH_BYTES, &p)) return DCP_ERR_WORKSPACE_TOO_SMALL;

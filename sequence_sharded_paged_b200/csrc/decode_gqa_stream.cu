@@ -1,0 +1,1099 @@
+// decode_gqa_stream.cu -- GQA decode attention in which every warp streams its own
+// part of the cache: over 4-bit caches (all decode calls) and under a sliding
+// window with sinks (bf16 and 4-bit caches), for any group size and query length.
+//
+// "Efficient Decode Context Parallelism with vLLM for Long Context Workloads",
+// section 4.1 ("Compute" on the local KV slice, partial output + LSE, and their
+// LSE-weighted sum) and section 5.4 (each KV head broadcast to its query heads).
+//
+// Mathematics: s = scale q.k, p = exp(s - m), l = sum p, O = sum p v / l over the
+// visible positions, in one pass with a running reference m.  m moves only when a
+// row's maximum grows by more than 2^8 (lazy rescale).
+//
+// Work: a segment is (request, KV head, tile of 16 query rows) -- of one shard when
+// partials are asked for, of all shards otherwise.  Its visible local positions are
+// read in groups of 16 tokens; a group never leaves its page.  A team of 1 or 4
+// warps takes whole segments (short windows: one launch, nothing to merge), or an
+// equal share of the flat list of all groups, whatever the lengths; the two ends of
+// a share may then be parts of a segment, whose (O, LSE) go to the workspace and are
+// summed by combine_kernel.
+//
+// Tile: 16 query rows x 16 tokens on mma.sync m16n8k16 with fp32 accumulators.  Only
+// one token is read for 16 query rows at most, so the tensor pipe is far from its
+// limit and what counts is that the bytes arrive in the layout in which the
+// instruction wants them.  The dimensions of a k-step and the tokens of a group may
+// be permuted freely (Q, and P from S, are permuted alike), so each thread takes 16
+// (4-bit: 16 or 8) CONSECUTIVE bytes of a row as its operands:
+//   Q K^T  thread (n = lane / 4, c = lane % 4), token tile t: token
+//          4 (n >> 1) + 2 t + (n & 1); dimensions 32 c .. (4-bit) or
+//          32 i + 8 c .. + 7 (bf16, i-th 16 bytes);
+//   P V    thread (n, c): tokens 4 c .. 4 c + 3, dimensions n D/8 .. + D/8 - 1 (n-tile
+//          j is dimension n D/8 + j); S leaves tokens 4 c .. 4 c + 3 in thread c.
+// So no data is exchanged between threads: every thread copies (cp.async) exactly the
+// bytes it will use into its own slots of a shared-memory queue, several groups ahead,
+// and the only wait in the kernel is the thread's own cp.async.wait_group.  Tokens
+// that no row may see are filled with zeros by the copy itself, so that stale or
+// non-finite bytes in masked places never meet a product.
+//
+// Precision: bf16 caches: Q K^T in bf16 (exact products), P in two bf16 terms (16
+// bits).  4-bit caches: code times scale has 6 significant bits and lies within
+// 2^-10 .. 2688, so it is exact in fp16; q is scaled by a power of two into fp16's
+// range; P in two fp16 terms, with the reference 2^7 below the maximum so that small
+// weights stay above fp16's smallest step.  With at most 8 query rows the two terms
+// share one instruction (rows 0..7 and 8..15 of the tile); with more they take two.
+#include <limits.h>
+
+#include "common.cuh"
+#include "finish.cuh"
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace dcp {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTok = 16;     // tokens per group
+constexpr int kDescs = 64;   // group descriptors per warp (two batches of 32)
+constexpr float kLazy = 8.f; // lazy rescale threshold (log2)
+
+// Launch constants of one cache type and head size.
+//   bf16: K 2 tiles x D/32 x 16 B, V 4 tokens x D/64 x 16 B a lane and group
+//   4-bit: K 2 tiles x D/8 B, V 4 tokens x D/16 B, scales (D/64 + 1) words
+template <bool FP4, int D>
+struct Lane {
+    static constexpr int kK = FP4 ? 2 * D / 8 : 2 * (D / 32) * 16;  // bytes of K
+    static constexpr int kV = FP4 ? 4 * D / 16 : 4 * (D / 64) * 16;
+    static constexpr int kS = FP4 ? (D / 64 + 1) * 4 : 0;
+    static constexpr int kStage = 32 * (kK + kV + kS);
+    // groups in the queue: as many as let three CTAs share an SM
+    static constexpr int kStages = FP4 ? (D == 128 ? 7 : 12) : (D == 128 ? 2 : 4);
+};
+
+struct StreamArgs {
+    const uint8_t* k_pages;
+    const uint8_t* v_pages;
+    const float* factors;  // 4-bit: {K, V} factors, or null
+    const int32_t* block_tables;
+    const __nv_bfloat16* q;
+    const int32_t* seq_lens;
+    float* out;
+    float* lse;
+    float* part_o;    // [2 * workers][16][D]
+    float* part_lse;  // [2 * workers][16], log2
+    int4* tail;       // [workers]: segment that starts in the worker's share and ends in another's
+    int* status;
+    int64_t* finish_ns;
+    const int64_t* t_start;
+    uint32_t in;  // interleave * n_shards, saturated
+    int32_t n_shards, interleave, page_size, num_pages, batch, max_local_pages;
+    int32_t hq, hkv, q_len, group, rows, tiles;
+    int32_t window, sinks;
+    int32_t shard_lo, shard_hi, per_shard, bt_shard0;
+    int32_t team;     // warps per team: 1 or kWarps
+    int32_t workers;  // teams in the grid
+    int32_t whole;    // whole segments, else equal shares
+    float scale_log2;
+};
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool FP4>
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    if (FP4)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the four bytes of w, two e2m1 values each, as four f16x2
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t* h) {
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {  // low two bytes -> f16x2, exact
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// x ~ hi + lo, two values, in the operand type
+template <bool FP4>
+__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+    if (FP4) {
+        const __half2 h = __floats2half2_rn(x0, x1);
+        const float2 f = __half22float2(h);
+        const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = *reinterpret_cast<const uint32_t*>(&l);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+        hi = *reinterpret_cast<const uint32_t*>(&h);
+        lo = *reinterpret_cast<const uint32_t*>(&l);
+    }
+}
+
+// positions p < x that shard n owns
+struct Counter {
+    uint32_t base, rest;
+    __device__ __forceinline__ Counter(uint32_t x, const StreamArgs& a) {
+        const uint32_t q = x / a.in;
+        base = q * (uint32_t)a.interleave;
+        rest = x - q * a.in;
+    }
+    __device__ __forceinline__ int of(int n, const StreamArgs& a) const {
+        const int64_t r = (int64_t)rest - (int64_t)n * a.interleave;
+        return (int)(base + (uint32_t)(r < 0 ? 0 : r > a.interleave ? a.interleave : r));
+    }
+};
+
+// What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
+// when the two meet).
+struct Visible {
+    int L, first;  // length, position of query token 0 (may be negative)
+    Counter cs, cl, ch;
+    __device__ __forceinline__ Visible(int len, const StreamArgs& a)
+        : L(len), first(len - a.q_len), cs(0, a), cl(0, a), ch((uint32_t)len, a) {
+        const int lo = a.window > first ? 0 : first - a.window + 1;
+        if (lo > a.sinks) {
+            cs = Counter((uint32_t)a.sinks, a);
+            cl = Counter((uint32_t)lo, a);
+        }
+    }
+    // shard n's groups: [0, sg) and [w0, w1)
+    __device__ __forceinline__ void groups(int n, const StreamArgs& a, int* sg, int* w0, int* w1) const {
+        *sg = (cs.of(n, a) + kTok - 1) / kTok;
+        *w0 = max(cl.of(n, a) / kTok, *sg);
+        *w1 = max((ch.of(n, a) + kTok - 1) / kTok, *w0);
+    }
+};
+
+__device__ __forceinline__ int length_of(const StreamArgs& a, int b) { return max(0, __ldg(a.seq_lens + b)); }
+
+// groups of base (block of shards, request); at least 1, so that every row is written
+__device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
+    const int blk = base / a.batch;
+    const Visible v(length_of(a, base - blk * a.batch), a);
+    const int lo = a.per_shard ? a.shard_lo + blk : a.shard_lo, hi = a.per_shard ? lo + 1 : a.shard_hi;
+    int g = 0;
+    for (int n = lo; n < hi; n++) {
+        int sg, w0, w1;
+        v.groups(n, a, &sg, &w0, &w1);
+        g += sg + w1 - w0;
+    }
+    return max(g, 1);
+}
+
+// A group: its page (-1: none), first local token, shard, and whether every row
+// sees all of it.
+struct Desc {
+    int page, t0, shard, full;
+};
+
+__device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
+    const uint32_t q = (uint32_t)t / (uint32_t)a.interleave;
+    return (int64_t)q * a.in + (int64_t)shard * a.interleave + (t - (int)(q * (uint32_t)a.interleave));
+}
+
+__device__ __forceinline__ bool sees(const StreamArgs& a, int64_t p, int at) {
+    return p <= at && (p < a.sinks || at - p < a.window);
+}
+
+// Everything a warp keeps for the segment it works on.
+template <bool FP4, int D, bool HALF>
+struct Warp {
+    static constexpr int KS = D / 16;  // k-steps of Q K^T
+    static constexpr int NT = D / 8;   // n-tiles of P V
+    using C = Lane<FP4, D>;
+    static constexpr float kBias = FP4 ? 7.f : 0.f;
+
+    uint32_t q[KS][HALF ? 2 : 4];
+    float o[NT][4];
+    float m[2], l[2], scale[2];
+    int at[2];  // positions of rows qr and qr + 8
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int j = 0; j < NT; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    // Q fragments of rows qr (and qr + 8) of tile `tile` of KV head g
+    __device__ __forceinline__ void load_q(const StreamArgs& a, int b, int g, int tile, int L, float kf) {
+        const int lane = threadIdx.x & 31, qr = lane >> 2, c = lane & 3;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const int r = tile * 16 + qr + 8 * h;
+            const bool live = r < a.rows && !(HALF && h);
+            const int j = live ? r / a.group : 0, hh = live ? r - j * a.group : 0;
+            at[h] = live ? L - a.q_len + j : INT_MIN / 2;
+            scale[h] = a.scale_log2;
+            if (HALF && h) continue;
+            const uint2* src = reinterpret_cast<const uint2*>(
+                a.q + (((int64_t)b * a.q_len + j) * a.hq + g * a.group + hh) * D);  // 4 dimensions each
+            uint2 w[KS];
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                const int d4 = FP4 ? (D / 4 * c) / 4 + s : (s >> 1) * 8 + c * 2 + (s & 1);
+                w[s] = live ? __ldg(src + d4) : make_uint2(0, 0);
+            }
+            if (FP4) {
+                // a power of two brings the row's largest magnitude into [1, 2)
+                float amax = 0.f;
+#pragma unroll
+                for (int s = 0; s < KS; s++)
+                    amax = fmaxf(fmaxf(amax, fmaxf(fabsf(bf16_lo(w[s].x)), fabsf(bf16_hi(w[s].x)))),
+                                 fmaxf(fabsf(bf16_lo(w[s].y)), fabsf(bf16_hi(w[s].y))));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                int e = (int)(__float_as_uint(amax) >> 23) - 127;
+                e = (e > 127 || amax == 0.f) ? 0 : min(126, max(-126, e));
+                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+                scale[h] = a.scale_log2 * kf * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                for (int s = 0; s < KS; s++) {
+                    const __half2 x = __floats2half2_rn(bf16_lo(w[s].x) * f, bf16_hi(w[s].x) * f);
+                    const __half2 y = __floats2half2_rn(bf16_lo(w[s].y) * f, bf16_hi(w[s].y) * f);
+                    w[s].x = *reinterpret_cast<const uint32_t*>(&x);
+                    w[s].y = *reinterpret_cast<const uint32_t*>(&y);
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < KS; s++) {
+                if (HALF) {
+                    q[s][0] = w[s].x;
+                    q[s][1] = w[s].y;
+                } else {
+                    q[s][h] = w[s].x;
+                    q[s][h + 2] = w[s].y;
+                }
+            }
+        }
+    }
+
+    // Start the copies of group d of KV head g into queue slot `slot`.
+    __device__ __forceinline__ static void issue(const StreamArgs& a, const Desc& d, int g, int L, uint32_t slot) {
+        if (d.page < 0) return;
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        const int P = a.page_size, sub = d.t0 & (P - 1);
+        const int64_t blk = (int64_t)d.page * a.hkv + g;
+        const int kt = 4 * (n >> 1) + (n & 1);  // K: token of tile 0 (tile 1: + 2)
+        bool lk[2] = {true, true}, lv[4] = {true, true, true, true};
+        if (!d.full) {  // a token is copied if any query token sees it
+            const int first = L - a.q_len;
+#pragma unroll
+            for (int e = 0; e < 6; e++) {
+                const int64_t p = position_of(a, d.shard, d.t0 + (e < 2 ? kt + 2 * e : 4 * c + e - 2));
+                const bool any = p < L && (p < a.sinks || first - p < a.window);
+                if (e < 2)
+                    lk[e] = any;
+                else
+                    lv[e - 2] = any;
+            }
+        }
+        if (!FP4) {
+            const uint8_t* kb = a.k_pages + (blk * P + sub) * (D * 2) + kt * (D * 2) + c * 16;
+            const uint8_t* vb = a.v_pages + (blk * P + sub) * (D * 2) + 4 * c * (D * 2) + n * (D / 4);
+            const uint32_t dst = slot + lane * 16;
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int i = 0; i < D / 32; i++)
+                    cp16(dst + (t * (D / 32) + i) * 512, kb + t * 2 * (D * 2) + i * 64, lk[t]);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+#pragma unroll
+                for (int i = 0; i < D / 64; i++)
+                    cp16(dst + C::kK * 32 + (e * (D / 64) + i) * 512, vb + e * (D * 2) + i * 16, lv[e]);
+        } else {
+            const int64_t off = blk * fp4_block_bytes(P, D);
+            const uint8_t* kb = a.k_pages + off + (sub + kt) * (D / 2) + c * (D / 8);
+            const uint8_t* vb = a.v_pages + off + (sub + 4 * c) * (D / 2) + n * (D / 16);
+            const uint8_t* ks = a.k_pages + off + P * (D / 2) + (c * (D / 64)) * P + sub + 4 * (n >> 1);
+            const uint8_t* vs = a.v_pages + off + P * (D / 2) + (n * D / 128) * P + sub + 4 * c;
+            // scale words hold four tokens; a token that is not copied has zero codes
+            const uint32_t ds = slot + (C::kK + C::kV) * 32 + lane * 4;
+            if (D == 128) {
+                cp16(slot + lane * 16, kb, lk[0]);
+                cp16(slot + 512 + lane * 16, kb + 2 * (D / 2), lk[1]);
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    cp8(slot + 1024 + (e >> 1) * 512 + lane * 16 + (e & 1) * 8, vb + e * (D / 2), lv[e]);
+                cp4(ds, ks, true);
+                cp4(ds + 128, ks + P, true);
+                cp4(ds + 256, vs, true);
+            } else {
+                cp8(slot + lane * 16, kb, lk[0]);
+                cp8(slot + lane * 16 + 8, kb + 2 * (D / 2), lk[1]);
+#pragma unroll
+                for (int e = 0; e < 4; e++) cp4(slot + 512 + lane * 16 + e * 4, vb + e * (D / 2), lv[e]);
+                cp4(ds, ks, true);
+                cp4(ds + 128, vs, true);
+            }
+        }
+    }
+
+    // V operands of n-tiles 8 w .. 8 w + 7: b[j][0] tokens 4c, 4c+1; b[j][1] tokens 4c+2, 4c+3
+    __device__ __forceinline__ static void load_v(const uint8_t* slot, int w, uint32_t (*b)[2]) {
+        const int lane = threadIdx.x & 31;
+        if (!FP4) {
+            uint4 v[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[e] = *reinterpret_cast<const uint4*>(slot + C::kK * 32 + (e * (D / 64) + w) * 512 + lane * 16);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t x[4] = {v[2 * h].x, v[2 * h].y, v[2 * h].z, v[2 * h].w};
+                const uint32_t y[4] = {v[2 * h + 1].x, v[2 * h + 1].y, v[2 * h + 1].z, v[2 * h + 1].w};
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    b[2 * k][h] = __byte_perm(x[k], y[k], 0x5410);
+                    b[2 * k + 1][h] = __byte_perm(x[k], y[k], 0x7632);
+                }
+            }
+        } else {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                v[e] = D == 128 ? *reinterpret_cast<const uint32_t*>(slot + 1024 + (e >> 1) * 512 + lane * 16 +
+                                                                     (e & 1) * 8 + w * 4)
+                                : *reinterpret_cast<const uint32_t*>(slot + 512 + lane * 16 + e * 4);
+            const uint32_t sw =
+                *reinterpret_cast<const uint32_t*>(slot + (C::kK + C::kV) * 32 + (D / 64) * 128 + lane * 4);
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                // low half of a byte: token 4c + 2h, high half: the next token, same dimension
+                const uint32_t x = v[2 * h], y = v[2 * h + 1];
+                const uint32_t s = e4m3x2(h ? sw >> 16 : sw & 0xffffu);
+                uint32_t even[4], odd[4];
+                e2m1x8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), even);
+                e2m1x8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd);
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    b[2 * k][h] = mul2(even[k], s);
+                    b[2 * k + 1][h] = mul2(odd[k], s);
+                }
+            }
+        }
+    }
+
+    // One group: scores, softmax step, O += P V.
+    __device__ __forceinline__ void consume(const StreamArgs& a, const Desc& d, const uint8_t* slot) {
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        float x[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; t++) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
+        if (!FP4) {
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+#pragma unroll
+                for (int t = 0; t < 2; t++) {
+                    const uint4 k = *reinterpret_cast<const uint4*>(slot + (t * (D / 32) + i) * 512 + lane * 16);
+                    qk(x[t], 2 * i, k.x, k.y);
+                    qk(x[t], 2 * i + 1, k.z, k.w);
+                }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                uint32_t kw[D / 32];
+                if (D == 128) {
+                    const uint4 k = *reinterpret_cast<const uint4*>(slot + t * 512 + lane * 16);
+                    kw[0] = k.x, kw[1] = k.y, kw[D / 32 - 2] = k.z, kw[D / 32 - 1] = k.w;
+                } else {
+                    const uint2 k = *reinterpret_cast<const uint2*>(slot + lane * 16 + t * 8);
+                    kw[0] = k.x, kw[1] = k.y;
+                }
+                // this token's byte of the scale words, twice
+                const uint32_t sel = (uint32_t)(2 * t + (n & 1)) * 0x11u;
+#pragma unroll
+                for (int w = 0; w < D / 32; w++) {
+                    const uint32_t sw = *reinterpret_cast<const uint32_t*>(slot + (C::kK + C::kV) * 32 +
+                                                                           (w >> 1) * 128 + lane * 4);
+                    const uint32_t s = e4m3x2(__byte_perm(sw, 0, sel));
+                    uint32_t h[4];
+                    e2m1x8(kw[w], h);
+                    qk(x[t], 2 * w, mul2(h[0], s), mul2(h[1], s));
+                    qk(x[t], 2 * w + 1, mul2(h[2], s), mul2(h[3], s));
+                }
+            }
+        }
+        bool vis[2][4];  // [row][token 4c + e]
+        if (!d.full) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t p = position_of(a, d.shard, d.t0 + 4 * c + e);
+                vis[0][e] = sees(a, p, at[0]);
+                vis[1][e] = sees(a, p, at[1]);
+            }
+        }
+        // x[t][e], e = 0, 1: row qr, token 4c + 2t + e; e = 2, 3: row qr + 8
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int e = 0; e < (HALF ? 2 : 4); e++) {
+                x[t][e] *= scale[e >> 1];
+                if (!d.full && !vis[e >> 1][2 * t + (e & 1)]) x[t][e] = -INFINITY;
+                mx[e >> 1] = fmaxf(mx[e >> 1], x[t][e]);
+            }
+        const bool grow = mx[0] > m[0] + (kLazy + kBias) || (!HALF && mx[1] > m[1] + (kLazy + kBias));
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int h = 0; h < (HALF ? 1 : 2); h++) {
+                float t = mx[h];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                if (t > m[h] + (kLazy + kBias)) {
+                    const float mn = t - kBias;
+                    const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
+                    m[h] = mn;
+                    l[h] *= f;
+#pragma unroll
+                    for (int j = 0; j < NT; j++) {
+                        o[j][2 * h] *= f;
+                        o[j][2 * h + 1] *= f;
+                        if (HALF) {
+                            o[j][2] *= f;
+                            o[j][3] *= f;
+                        }
+                    }
+                }
+            }
+        }
+        uint32_t hi[4], lo[4];  // A operands: [row half + 2 * tile]
+#pragma unroll
+        for (int h = 0; h < (HALF ? 1 : 2); h++) {
+            const float ref = m[h] == -INFINITY ? 0.f : m[h];
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                const float p0 = fast_exp2(x[t][2 * h] - ref), p1 = fast_exp2(x[t][2 * h + 1] - ref);
+                l[h] += p0 + p1;
+                split2<FP4>(p0, p1, hi[h + 2 * t], lo[h + 2 * t]);
+            }
+        }
+        if (HALF) {  // rows 8..15 carry the low terms
+            hi[1] = lo[0];
+            hi[3] = lo[2];
+        }
+        if (!d.full && a.q_len > 1 && poisoned(slot)) {
+            careful(a, d, slot, hi, lo, vis);
+            return;
+        }
+#pragma unroll
+        for (int w = 0; w < NT / 8; w++) {
+            uint32_t b[8][2];
+            load_v(slot, w, b);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                mma<FP4>(o[8 * w + j], hi[0], hi[1], hi[2], hi[3], b[j][0], b[j][1]);
+                if (!HALF) mma<FP4>(o[8 * w + j], lo[0], lo[1], lo[2], lo[3], b[j][0], b[j][1]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void qk(float* d, int s, uint32_t b0, uint32_t b1) {
+        if (HALF)
+            mma<FP4>(d, q[s][0], 0u, q[s][1], 0u, b0, b1);
+        else
+            mma<FP4>(d, q[s][0], q[s][1], q[s][HALF ? 0 : 2], q[s][HALF ? 0 : 3], b0, b1);
+    }
+
+    // Does the group hold an infinity or NaN among its values?
+    __device__ __forceinline__ static bool poisoned(const uint8_t* slot) {
+        bool bad = false;
+#pragma unroll 1
+        for (int w = 0; w < NT / 8; w++) {
+            uint32_t b[8][2];
+            load_v(slot, w, b);
+            constexpr uint32_t e = FP4 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    bad |= (b[j][h] & e) == e || ((b[j][h] >> 16) & e) == e;
+        }
+        return __any_sync(0xffffffffu, bad);
+    }
+
+    // P V where some rows must not see a non-finite value that others see: row by
+    // row, with the values that the row does not see set to zero.
+    __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot, const uint32_t* hi,
+                                         const uint32_t* lo, bool (*vis)[4]) {
+        const int lane = threadIdx.x & 31, qr = lane >> 2;
+#pragma unroll 1
+        for (int r = 0; r < (HALF ? 8 : 16); r++) {
+            // the position of row r, from a lane that holds it
+            const int at_r = __shfl_sync(0xffffffffu, r < 8 ? at[0] : at[1], (r & 7) * 4);
+            uint32_t keep[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                keep[h] = 0;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    const int64_t p = position_of(a, d.shard, d.t0 + 4 * (lane & 3) + 2 * h + e);
+                    if (sees(a, p, at_r)) keep[h] |= 0xffffu << (16 * e);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NT / 8; w++) {
+                uint32_t b[8][2];
+                load_v(slot, w, b);
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    float t[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma<FP4>(t, hi[0], hi[1], hi[2], hi[3], b[j][0] & keep[0], b[j][1] & keep[1]);
+                    if (!HALF) mma<FP4>(t, lo[0], lo[1], lo[2], lo[3], b[j][0] & keep[0], b[j][1] & keep[1]);
+                    if (qr == (r & 7)) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            if (HALF || (e >> 1) == (r >> 3)) o[8 * w + j][e] += t[e];
+                    }
+                }
+            }
+        }
+    }
+
+    // After the last group: whole-row sums, the low terms folded in, l and m the same
+    // in the row's four lanes.
+    __device__ __forceinline__ void close() {
+#pragma unroll
+        for (int h = 0; h < (HALF ? 1 : 2); h++) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+        if (HALF) {
+#pragma unroll
+            for (int j = 0; j < NT; j++) {
+                o[j][0] += o[j][2];
+                o[j][1] += o[j][3];
+            }
+        }
+    }
+};
+
+// Where a row of a segment goes.
+struct Row {
+    float* o;
+    float* lse;
+};
+
+// Output row r of segment (base, g, tile): the caller's tensors.
+__device__ __forceinline__ Row out_row(const StreamArgs& a, int base, int g, int tile, int r, int D) {
+    const int rr = tile * 16 + r, j = rr / a.group, h = rr - j * a.group;
+    const int64_t at = ((int64_t)base * a.q_len + j) * a.hq + g * a.group + h;
+    return Row{a.out + at * D, a.lse + at};
+}
+
+// min blocks per SM: three CTAs of four warps at 168 registers
+template <bool FP4, int D, bool HALF>
+__global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
+    using W = Warp<FP4, D, HALF>;
+    using C = Lane<FP4, D>;
+    constexpr int S = C::kStages;
+    constexpr int kRing = S * C::kStage;
+    constexpr int kRows = HALF ? 8 : 16;
+    constexpr int kPitch = D + 4;  // floats a row of O in the team merge
+    static_assert(kRing >= kRows * kPitch * 4, "a warp's queue holds its O");
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ Desc s_desc[kWarps][kDescs];
+    __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+    __shared__ long long s_scan[kWarps];
+    __shared__ int s_base[kWarps], s_off[kWarps];  // per team: where its share begins
+    __shared__ int s_sub[kWarps];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int team = warp / a.team, wt = warp - team * a.team;  // team of the CTA, warp of the team
+    const int teams = kWarps / a.team;
+    const int worker = blockIdx.x * teams + team;
+    uint8_t* ring = smem + (size_t)warp * kRing;
+    const uint32_t ring_u32 = smem_u32(ring);
+    Desc* descs = s_desc[warp];
+    const int nb = (a.per_shard ? a.shard_hi - a.shard_lo : 1) * a.batch;
+    const int per_base = a.hkv * a.tiles;
+    const float kf = FP4 && a.factors ? __ldg(a.factors) : 1.f, vf = FP4 && a.factors ? __ldg(a.factors + 1) : 1.f;
+
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b < a.batch; b += kThreads) {
+            const int L = __ldg(a.seq_lens + b);
+            if (L < 0 || (L > 0 && L < a.q_len)) record_status(a.status, DCP_ERR_INVALID_ARG);
+        }
+
+    // this worker's share: segments [seg, ..) step `workers`, or flat groups [r0, r1)
+    long long r0 = 0, r1 = 0, total = 0;
+    int active = a.workers;
+    int base = 0, sub = 0, i0 = 0;
+    if (!a.whole) {
+        // every CTA sums all bases' groups, a run of consecutive bases for each thread
+        const int each = (nb + kThreads - 1) / kThreads;
+        const int b0 = min(nb, (int)threadIdx.x * each), b1 = min(nb, b0 + each);
+        long long mine = 0;
+        for (int b = b0; b < b1; b++) mine += (long long)base_groups(a, b) * per_base;
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += t;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) incl += s_scan[w];
+            total += s_scan[w];
+        }
+        // no share below 8 groups a warp: a partial costs about as much as those
+        const long long least = 8ll * a.team;
+        active = (int)min((long long)a.workers, (total + least - 1) / least);
+        for (int t = 0; t < teams; t++) {
+            const int w = blockIdx.x * teams + t;
+            if (w >= active) break;
+            long long at = total * w / active - (incl - mine);
+            if (at < 0 || at >= mine) continue;
+            for (int b = b0; b < b1; b++) {
+                const int g = base_groups(a, b);
+                const long long size = (long long)g * per_base;
+                if (at < size) {
+                    s_base[t] = b;
+                    s_sub[t] = (int)(at / g);
+                    s_off[t] = (int)(at % g);
+                    break;
+                }
+                at -= size;
+            }
+        }
+        __syncthreads();
+        if (worker < active) {
+            r0 = total * worker / active;
+            r1 = total * (worker + 1) / active;
+            base = s_base[team];
+            sub = s_sub[team];
+            i0 = s_off[team];
+        }
+    }
+    int4 tail = make_int4(-1, 0, 0, 0);
+    long long pos = r0;
+    long long seg = worker;
+    W st;
+
+    auto team_sync = [&]() {
+        if (a.team == 1)
+            __syncwarp();
+        else
+            __syncthreads();
+    };
+
+    while (a.whole ? seg < (long long)nb * per_base : pos < r1) {
+        if (a.whole) {
+            base = (int)(seg / per_base);
+            sub = (int)(seg - (long long)base * per_base);
+            i0 = 0;
+        }
+        const int blk = base / a.batch, b = base - blk * a.batch;
+        const int g = sub / a.tiles, tile = sub - g * a.tiles;
+        const int lo = a.per_shard ? a.shard_lo + blk : a.shard_lo, hi = a.per_shard ? lo + 1 : a.shard_hi;
+        const int L = length_of(a, b);
+        const Visible v(L, a);
+        int ng = 0;
+        for (int n = lo; n < hi; n++) {
+            int sg, w0, w1;
+            v.groups(n, a, &sg, &w0, &w1);
+            ng += sg + w1 - w0;
+        }
+        const int real = ng;  // 0: nothing visible, one empty group
+        ng = max(ng, 1);
+        const int take = a.whole ? ng : (int)min((long long)(ng - i0), r1 - pos);
+        const int nk = wt < take ? (take - wt + a.team - 1) / a.team : 0;  // this warp's groups
+
+        // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
+        auto batch = [&](int kb) {
+            const int k = 32 * kb + lane;
+            Desc d{-1, 0, 0, 0};
+            int i = i0 + wt + a.team * k;
+            if (k < nk && i < real) {
+                for (int n = lo; n < hi; n++) {
+                    int sg, w0, w1;
+                    v.groups(n, a, &sg, &w0, &w1);
+                    if (i < sg + w1 - w0) {
+                        d.shard = n;
+                        d.t0 = kTok * (i < sg ? i : w0 + i - sg);
+                        break;
+                    }
+                    i -= sg + w1 - w0;
+                }
+                const int j = d.t0 / a.page_size;
+                int pg = -1;
+                if (j < a.max_local_pages)
+                    pg = __ldg(a.block_tables + ((int64_t)(d.shard - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
+                if (pg < 0 || pg >= a.num_pages)
+                    record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
+                else
+                    d.page = pg;
+                const int64_t p0 = position_of(a, d.shard, d.t0), p1 = position_of(a, d.shard, d.t0 + kTok - 1);
+                d.full = p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p0 < a.window);
+            }
+            __syncwarp();
+            descs[(kb & 1) * 32 + lane] = d;
+            __syncwarp();
+        };
+
+        if (nk > 0) batch(0);
+#pragma unroll
+        for (int k = 0; k < S - 1; k++) {
+            if (k < nk) W::issue(a, descs[k], g, L, ring_u32 + k * C::kStage);
+            cp_commit();
+        }
+        st.reset();
+        st.load_q(a, b, g, tile, L, kf);
+        int slot_in = S - 1, slot_out = 0;
+        for (int k = 0; k < nk; k++) {
+            const int f = k + S - 1;
+            if (f < nk) {
+                if ((f & 31) == 0) batch(f >> 5);
+                W::issue(a, descs[f & (kDescs - 1)], g, L, ring_u32 + slot_in * C::kStage);
+            }
+            cp_commit();
+            if (++slot_in == S) slot_in = 0;
+            cp_wait<S - 1>();
+            const Desc d = descs[k & (kDescs - 1)];
+            if (d.page >= 0) st.consume(a, d, ring + slot_out * C::kStage);
+            if (++slot_out == S) slot_out = 0;
+        }
+        cp_wait<0>();
+        __syncwarp();  // the next segment's descriptors overwrite these
+        st.close();
+
+        // where the rows go: the caller's tensors, or a slot of the workspace
+        const bool starts = i0 == 0, ends = i0 + take == ng;
+        const bool final_rows = starts && ends;
+        const int part = 2 * worker + (starts ? 1 : 0);
+        const int rows = min(kRows, a.rows - tile * 16);
+        const int qr = lane >> 2, c = lane & 3;
+        auto put = [&](int r, int d, const float4& x) {  // 4 dimensions of row r
+            float* dst = final_rows ? out_row(a, base, g, tile, r, D).o : a.part_o + ((int64_t)part * 16 + r) * D;
+            *reinterpret_cast<float4*>(dst + d) = x;
+        };
+        auto put_lse = [&](int r, float lse2) {
+            if (final_rows)
+                *out_row(a, base, g, tile, r, D).lse = lse2 * kLn2;
+            else
+                a.part_lse[(int64_t)part * 16 + r] = lse2;
+        };
+        if (a.team == 1) {
+#pragma unroll
+            for (int h = 0; h < (HALF ? 1 : 2); h++) {
+                const int r = qr + 8 * h;
+                if (r < rows) {
+                    const float inv = st.l[h] == 0.f ? 0.f : vf / st.l[h];
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+#pragma unroll
+                        for (int j = 0; j < W::NT; j += 4)
+                            put(r, (2 * c + e) * W::NT + j,
+                                make_float4(st.o[j][2 * h + e] * inv, st.o[j + 1][2 * h + e] * inv,
+                                            st.o[j + 2][2 * h + e] * inv, st.o[j + 3][2 * h + e] * inv));
+                    if (c == 0) put_lse(r, st.l[h] == 0.f ? -INFINITY : (st.m[h] == -INFINITY ? 0.f : st.m[h]) + log2f(st.l[h]));
+                }
+            }
+        } else {
+            // the team's warps: each leaves its O in its own (drained) queue, then all
+            // threads sum the four with the weights of their references
+            float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+            for (int h = 0; h < (HALF ? 1 : 2); h++) {
+                const int r = qr + 8 * h;
+#pragma unroll
+                for (int e = 0; e < 2; e++)
+#pragma unroll
+                    for (int j = 0; j < W::NT; j += 4)
+                        *reinterpret_cast<float4*>(so + r * kPitch + (2 * c + e) * W::NT + j) =
+                            make_float4(st.o[j][2 * h + e], st.o[j + 1][2 * h + e], st.o[j + 2][2 * h + e],
+                                        st.o[j + 3][2 * h + e]);
+                if (c == 0) {
+                    s_m[warp][r] = st.m[h];
+                    s_l[warp][r] = st.l[h];
+                }
+            }
+            __syncthreads();
+            for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
+                const int r = k / (D / 4), d = (k - r * (D / 4)) * 4;
+                float M = -INFINITY, ls = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][r]);
+                const float ref = M == -INFINITY ? 0.f : M;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) {
+                    if (s_l[w][r] == 0.f) continue;
+                    const float f = s_m[w][r] == -INFINITY ? 1.f : fast_exp2(s_m[w][r] - ref);
+                    const float4 x = *reinterpret_cast<const float4*>(
+                        reinterpret_cast<const float*>(smem + (size_t)w * kRing) + r * kPitch + d);
+                    ls = fmaf(f, s_l[w][r], ls);
+                    acc.x = fmaf(f, x.x, acc.x);
+                    acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z);
+                    acc.w = fmaf(f, x.w, acc.w);
+                }
+                const float inv = ls == 0.f ? 0.f : vf / ls;
+                put(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                if (d == 0) put_lse(r, ls == 0.f ? -INFINITY : ref + log2f(ls));
+            }
+        }
+        if (a.finish_ns) {
+            team_sync();
+            if (wt == 0 && lane == 0) {
+                const uint64_t dt = global_timer_ns() - (uint64_t)*a.t_start;
+                atomicMax(reinterpret_cast<unsigned long long*>(a.finish_ns + b), (unsigned long long)dt);
+            }
+        }
+        if (!a.whole && starts && !ends) {
+            // the worker whose share holds the segment's last group
+            const long long e = pos + ng;  // one past it
+            tail = make_int4(base, sub, (int)((e * active + total - 1) / total) - 1, 0);
+        }
+        team_sync();  // queues and s_m are free again
+        if (a.whole) {
+            seg += a.workers;
+        } else {
+            pos += take;
+            i0 = 0;
+            if (++sub == per_base) {
+                sub = 0;
+                base++;
+            }
+        }
+    }
+    if (!a.whole && wt == 0 && lane == 0) a.tail[worker] = tail;
+}
+
+// Sum of a segment's parts: worker w's tail and the heads of the workers after it up
+// to tail[w].z.  CTA (w, block of rows); `wpr` warps share a row's parts.
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ StreamArgs a, int D, int wpr) {
+    const int4 t = a.tail[blockIdx.x];
+    if (t.x < 0) return;
+    __shared__ float s_w[8];
+    __shared__ float4 s_o[8][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rpc = 8 / wpr;
+    const int r = blockIdx.y * rpc + warp / wpr, part = warp % wpr;
+    const int g = t.y / a.tiles, tile = t.y - g * a.tiles;
+    const bool live = r < min(16, a.rows - tile * 16);
+    const int K = t.z - (int)blockIdx.x + 1;  // parts
+    const int nv = D / 4;
+    // part k's slot: the tail of the first worker, the heads of the others
+    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * 16 + r; };
+    float M = -INFINITY, ws = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (live) {
+        for (int k = lane; k < K; k += 32) M = fmaxf(M, __ldg(a.part_lse + slot(k)));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+        for (int k = part; k < K; k += wpr) {
+            const float e = __ldg(a.part_lse + slot(k));
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (lane < nv) x = __ldg(reinterpret_cast<const float4*>(a.part_o + slot(k) * D) + lane);
+            const float w = e == -INFINITY ? 0.f : exp2f(e - ref);
+            ws += w;
+            acc.x = fmaf(w, x.x, acc.x);
+            acc.y = fmaf(w, x.y, acc.y);
+            acc.z = fmaf(w, x.z, acc.z);
+            acc.w = fmaf(w, x.w, acc.w);
+        }
+    }
+    s_w[warp] = ws;
+    s_o[warp][lane] = acc;
+    __syncthreads();
+    if (!live || part != 0) return;
+    for (int w = 1; w < wpr; w++) {
+        const float4 x = s_o[warp + w][lane];
+        ws += s_w[warp + w];
+        acc.x += x.x;
+        acc.y += x.y;
+        acc.z += x.z;
+        acc.w += x.w;
+    }
+    const float inv = ws == 0.f ? 0.f : 1.f / ws;
+    const Row row = out_row(a, t.x, g, tile, r, D);
+    if (lane < nv) reinterpret_cast<float4*>(row.o)[lane] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (lane == 0) *row.lse = ws == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(ws)) * kLn2;
+}
+
+__global__ void finish_init_kernel(int64_t* finish_ns, int64_t* t_start, int B) {
+    for (int b = threadIdx.x; b < B; b += blockDim.x) finish_ns[b] = 0;
+    if (threadIdx.x == 0) *t_start = (int64_t)global_timer_ns();
+}
+
+template <bool FP4, int D, bool HALF>
+cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
+    constexpr int smem = kWarps * Lane<FP4, D>::kStages * Lane<FP4, D>::kStage;
+    // once per process and device would do; the call is cheap and keeps no state
+    cudaError_t e = cudaFuncSetAttribute(gqa_stream_kernel<FP4, D, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    gqa_stream_kernel<FP4, D, HALF><<<ctas, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+constexpr int kCtasPerSm = 3;  // of the launch bounds and the queues' sizes
+
+}  // namespace
+
+bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
+    return (dk == 64 || dk == 128) && hq % hkv == 0 && q_len >= 1;
+}
+
+// Splitting rule.  In units of one group's work by one warp: whole segments cost
+// rounds * groups of the longest segment, equal shares cost the mean share plus the
+// scan of the lengths, the partials and a second kernel.
+StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
+                           int num_sms) {
+    StreamPlan p;
+    const int64_t rows = (int64_t)q_len * (c->hq / c->hkv);
+    const int64_t segs = (int64_t)(per_shard ? shards : 1) * c->batch * c->hkv * ((rows + 15) / 16);
+    const int64_t span = per_shard ? 1 : shards;
+    // longest segment the tables and the mask allow; a shard's part starts and ends inside a group
+    int64_t tokens = (int64_t)c->max_local_pages * c->page_size * shards;
+    if (window != INT_MAX) {
+        const int64_t seen = (int64_t)sinks + window + q_len - 1;
+        if (seen < tokens) tokens = seen;
+    }
+    const int64_t groups = (tokens / shards + kTok - 1) / kTok * span + 2 * span;
+    const int64_t warps = (int64_t)num_sms * kCtasPerSm * kWarps, ctas = (int64_t)num_sms * kCtasPerSm;
+    const int64_t one = (segs + warps - 1) / warps * groups;
+    const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
+    const int64_t share = (segs * groups + warps - 1) / warps + 40;
+    p.team = 1;
+    p.whole = 1;
+    int64_t best = one;
+    if (four < best) {
+        best = four;
+        p.team = kWarps;
+    }
+    if (share < best) {
+        p.whole = 0;
+        p.team = 2 * segs >= warps ? 1 : kWarps;
+    }
+    int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
+    if (grid > ctas) grid = ctas;
+    p.ctas = (int)grid;
+    p.workers = p.ctas * (kWarps / p.team);
+    p.off_start = 0;
+    p.off_tail = 256;
+    size_t o = p.off_tail;
+    if (!p.whole) {
+        o = align256(o + sizeof(int4) * (size_t)p.workers);
+        p.off_lse = o;
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * 16);
+        p.off_o = o;
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * 16 * c->dk);
+    }
+    p.total = o;
+    return p;
+}
+
+cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int q_len, int window, int sinks,
+                              int shard_lo, int shard_hi, bool per_shard, int bt_shard0, const void* q,
+                              const int32_t* seq_lens, float* out, float* lse, int64_t* finish_ns, void* ws,
+                              int* status, cudaStream_t s) {
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    StreamArgs a;
+    a.k_pages = static_cast<const uint8_t*>(c->k_pages);
+    a.v_pages = static_cast<const uint8_t*>(c->v_pages);
+    a.factors = c->dtype == DCP_FP4_E2M1 ? c->kv_scales : nullptr;
+    a.block_tables = c->block_tables;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.seq_lens = seq_lens;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = p.whole ? nullptr : reinterpret_cast<float*>(w + p.off_o);
+    a.part_lse = p.whole ? nullptr : reinterpret_cast<float*>(w + p.off_lse);
+    a.tail = p.whole ? nullptr : reinterpret_cast<int4*>(w + p.off_tail);
+    a.status = status;
+    a.finish_ns = finish_ns;
+    a.t_start = reinterpret_cast<int64_t*>(w + p.off_start);
+    const uint64_t in = (uint64_t)c->interleave * (uint64_t)c->n_shards;
+    a.in = in > 0xffffffffu ? 0xffffffffu : (uint32_t)in;
+    a.n_shards = c->n_shards;
+    a.interleave = c->interleave;
+    a.page_size = c->page_size;
+    a.num_pages = c->num_pages;
+    a.batch = c->batch;
+    a.max_local_pages = c->max_local_pages;
+    a.hq = c->hq;
+    a.hkv = c->hkv;
+    a.q_len = q_len;
+    a.group = c->hq / c->hkv;
+    a.rows = q_len * a.group;
+    a.tiles = (a.rows + 15) / 16;
+    a.window = window;
+    a.sinks = sinks;
+    a.shard_lo = shard_lo;
+    a.shard_hi = shard_hi;
+    a.per_shard = per_shard;
+    a.bt_shard0 = bt_shard0;
+    a.team = p.team;
+    a.workers = p.workers;
+    a.whole = p.whole;
+    a.scale_log2 = c->scale * kLog2e;
+    if (finish_ns) {
+        finish_init_kernel<<<1, 256, 0, s>>>(finish_ns, reinterpret_cast<int64_t*>(w + p.off_start), c->batch);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    const bool fp4 = c->dtype == DCP_FP4_E2M1, half = a.rows <= 8;
+    cudaError_t e;
+    if (c->dk == 64) {
+        if (fp4)
+            e = half ? run<true, 64, true>(a, p.ctas, s) : run<true, 64, false>(a, p.ctas, s);
+        else
+            e = half ? run<false, 64, true>(a, p.ctas, s) : run<false, 64, false>(a, p.ctas, s);
+    } else {
+        if (fp4)
+            e = half ? run<true, 128, true>(a, p.ctas, s) : run<true, 128, false>(a, p.ctas, s);
+        else
+            e = half ? run<false, 128, true>(a, p.ctas, s) : run<false, 128, false>(a, p.ctas, s);
+    }
+    if (e != cudaSuccess || p.whole) return e;
+    // few teams a segment: a row for each warp; many: a CTA for each row
+    const int wpr = p.team == 1 ? 1 : 8;
+    const int rows = a.rows < 16 ? a.rows : 16;
+    combine_kernel<<<dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr))), 256, 0, s>>>(a, c->dk, wpr);
+    return cudaGetLastError();
+}
+
+}  // namespace dcp

@@ -34,6 +34,12 @@ cudaError_t launch_shard_map(int64_t n_pos, const int32_t* pos, const int32_t* r
                              int32_t* local_out, int64_t* slot_out, int* status, cudaStream_t s);
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 
+cudaError_t launch_gather(const AppendArgs& a, void* k_out, void* v_out, cudaStream_t s);
+// norms, rotation and append in one pass; a.k_new / a.v_new are rows k_stride / v_stride elements apart
+cudaError_t launch_norm_rope_append(const AppendArgs& a, const dcp_rope* rope, const void* q, int64_t q_stride,
+                                    int64_t k_stride, int64_t v_stride, const void* q_weight, const void* k_weight,
+                                    float eps, void* q_out, int hq, int num_sms, cudaStream_t s);
+
 // planner: splits every (shard, request) of shards [shard_lo, shard_hi) into
 // chunks of at most chunk_tokens; output row block of shard n of request b:
 // (n - shard_lo) * B + b
@@ -64,6 +70,21 @@ cudaError_t launch_decode_gqa_mma(const DecodeGeometry& g, const DecodeArgs& a, 
 bool mla_umma_supported(int hq, int page_size);
 cudaError_t launch_decode_mla_bf16(const DecodeGeometry& g, const DecodeArgs& a, cudaStream_t s);
 cudaError_t launch_decode_mla_fp8(const DecodeGeometry& g, const DecodeArgs& a, cudaStream_t s);
+
+// warp-streamed GQA decode (4-bit caches; sliding window with sinks)
+struct StreamPlan {
+    int team, whole;  // warps per team; whole segments or equal shares of all groups
+    int ctas, workers;
+    size_t off_start, off_tail, off_lse, off_o, total;  // workspace
+};
+bool gqa_stream_supported(int hq, int hkv, int dk, int q_len);
+// shards: how many are decoded; per_shard: a partial for each, else their sum
+StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
+                           int num_sms);
+cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int q_len, int window, int sinks,
+                              int shard_lo, int shard_hi, bool per_shard, int bt_shard0, const void* q,
+                              const int32_t* seq_lens, float* out, float* lse, int64_t* finish_ns, void* ws,
+                              int* status, cudaStream_t s);
 
 // discard != 0: o_partial is scratch whose lines are dropped from L2 once read
 cudaError_t launch_merge(int N, int B, int H, int Dv, const float* o_partial, const float* lse, float* out,

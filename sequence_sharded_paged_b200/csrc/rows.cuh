@@ -1,0 +1,127 @@
+// rows.cuh -- one token's row in its owner's page: where it lies and, for the
+// 4-bit and fp8 caches, how 8 consecutive values become codes.  Shared by the
+// append, read-back and norm-and-rotate kernels.
+//
+// Ownership follows "Efficient Decode Context Parallelism with vLLM for Long
+// Context Workloads", section 4, with the granularity of the "Decode Context
+// Parallel Guide"'s cp_kv_cache_interleave_size.
+#pragma once
+
+#include <cuda_fp4.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace dcp {
+
+// Bytes of a 4-bit block: one KV head's rows of one page, codes then scales.
+__host__ __device__ __forceinline__ int fp4_block_bytes(int P, int D) { return P * (D / 2 + D / 16); }
+
+// Resolve (req, pos) -> physical page and in-page offset; -1 page when invalid,
+// -2 when another rank owns the position (rank-local cache).
+__device__ __forceinline__ int append_target(const AppendArgs& a, int64_t i, int* off) {
+    const int p = a.pos[i];
+    int b = a.req ? a.req[i] : (int)i;
+    if (p < 0 || b < 0 || b >= a.batch) return -1;
+    // positions are below 2^31, so unsigned 32-bit division serves: p / (I N) = (p / I) / N
+    const uint32_t q = (uint32_t)p / (uint32_t)a.interleave;
+    const uint32_t round = q / (uint32_t)a.n_shards;
+    int r = (int)(q - round * (uint32_t)a.n_shards);
+    if (a.only_shard >= 0) {
+        if (r != a.only_shard) return -2;
+        r = 0;  // the rank's tables are row 0
+    }
+    const uint32_t l = round * (uint32_t)a.interleave + ((uint32_t)p - q * (uint32_t)a.interleave);
+    const int j = (int)(l / (uint32_t)a.page_size);
+    if (j >= a.max_local_pages) return -1;
+    int pg = a.block_tables[((int64_t)r * a.batch + b) * a.max_local_pages + j];
+    if (pg < 0 || pg >= a.num_pages) return -1;
+    *off = (int)(l % (uint32_t)a.page_size);
+    return pg;
+}
+
+// Quantise a run of 16 values held by two neighbouring lanes, 8 each: returns
+// this lane's 8 codes and the run's e4m3 scale byte.  factor > 0 multiplies
+// every scale.  `both` is the mask of the lanes that take part (whole pairs).
+// The scale is rounded up or down to e4m3 first and the codes are taken against
+// the rounded scale, so an element may lie past 6 and saturates there.
+__device__ __forceinline__ uint32_t fp4_quantise8(const float* x, float factor, uint32_t both, uint8_t* scale_byte) {
+    float amax = 0.f;
+    bool nan = false;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+        amax = fmaxf(amax, fabsf(x[e]));
+        nan |= x[e] != x[e];
+    }
+    float am = nan ? __int_as_float(0x7fc00000) : amax;
+    const float other = __shfl_xor_sync(both, am, 1);
+    am = (am != am || other != other) ? __int_as_float(0x7fc00000) : fmaxf(am, other);
+    const uint8_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(am, 6.f * factor), __NV_SATFINITE, __NV_E4M3);
+    const __half_raw hr = __nv_cvt_fp8_to_halfraw(sb, __NV_E4M3);
+    const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
+    uint32_t w = 0;
+    if (s > 0.f) {  // false for 0 and NaN: zero codes
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float2 y = make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
+            w |= (uint32_t)__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest) << (8 * e);
+        }
+    }
+    *scale_byte = sb;
+    return w;
+}
+
+// Codes of 8 values of an fp8 row whose largest magnitude is amax > 0.
+__device__ __forceinline__ uint2 fp8_quantise8(const float* x, float scale) {
+    uint32_t packed[2] = {0, 0};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const uint32_t b0 = __nv_cvt_float_to_fp8(__fdiv_rn(x[2 * e], scale), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t b1 = __nv_cvt_float_to_fp8(__fdiv_rn(x[2 * e + 1], scale), __NV_SATFINITE, __NV_E4M3);
+        packed[e >> 1] |= (b0 | (b1 << 8)) << (16 * (e & 1));
+    }
+    return make_uint2(packed[0], packed[1]);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        x[2 * e] = bf16_lo(ws[e]);
+        x[2 * e + 1] = bf16_hi(ws[e]);
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* x) {
+    uint4 w;
+    uint32_t* ws = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        ws[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return w;
+}
+
+// Store 8 values (dimensions 8 li .. 8 li + 7, bf16 in `w`) of KV head g's row at
+// (pg, off) of a GQA pool.  For a 4-bit pool every lane of `both` takes part in
+// the exchange of the runs' maxima; `live` says whether this lane stores.
+__device__ __forceinline__ void store_gqa8(const AppendArgs& a, uint8_t* pool, int pg, int g, int off, int li,
+                                           const uint4& w, float factor, uint32_t both, bool live) {
+    const int D = a.dk, P = a.page_size;
+    if (a.dtype == DCP_BF16) {
+        if (live)
+            *reinterpret_cast<uint4*>(pool + ((((int64_t)pg * a.hkv + g) * P + off) * D + li * 8) * 2) = w;
+        return;
+    }
+    float x[8];
+    unpack8(w, x);
+    uint8_t sb;
+    const uint32_t codes = fp4_quantise8(x, factor, both, &sb);
+    if (!live) return;
+    uint8_t* blk = pool + ((int64_t)pg * a.hkv + g) * fp4_block_bytes(P, D);
+    *reinterpret_cast<uint32_t*>(blk + off * (D / 2) + li * 4) = codes;
+    if ((li & 1) == 0) blk[P * (D / 2) + (li >> 1) * P + off] = sb;
+}
+
+}  // namespace dcp
