@@ -134,16 +134,16 @@ def status_string(status: int) -> str:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        device = _device()
+        if device >= 0:  # current_stream() builds a Stream object each time
+            return _torch._C._cuda_getCurrentRawStream(device)
+        return _torch.cuda.current_stream().cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -228,14 +228,25 @@ def dcp_lse_rescale(lse_all, rank: int, o, o_rs, lse_out=None, stream=None) -> N
                                  _stream(stream)), "dcp_lse_rescale")
 
 
-def _tensor(name: str, t, dtype: str, shape=None) -> None:
-    """Refuse a tensor whose layout the kernels would misread (torch tensors on the current device)."""
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+_torch = None  # the module, once a tensor has been checked
+
+
+def _device() -> int:
+    """The current device (a tensor on a GPU is at hand: torch has initialised CUDA)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
+
+
+def _tensor(name: str, t, device: int, dtype, shape=None) -> None:
+    """Refuse a tensor whose layout the kernels would misread."""
+    if t.get_device() != device or device < 0:
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    if t.dtype is not getattr(torch, dtype):
-        raise ValueError(f"{name} is {t.dtype}, not torch.{dtype}")
-    if shape is not None and (tuple(t.shape) != tuple(shape) or not t.is_contiguous()):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if shape is not None and (t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{name} is {tuple(t.shape)} (strides {t.stride()}), not a contiguous {tuple(shape)}")
 
 
@@ -243,11 +254,11 @@ def _rank(rank) -> int:
     return -1 if rank is None else int(rank)
 
 
-def _tokens(desc: CacheDesc, req, pos) -> int:
-    n = pos.numel()
-    _tensor("pos", pos, "int32", (n,))
+def _tokens(desc: CacheDesc, req, pos, device: int) -> int:
+    n = pos.shape[0]
+    _tensor("pos", pos, device, _torch.int32, (n,))
     if req is not None:
-        _tensor("req", req, "int32", (n,))
+        _tensor("req", req, device, _torch.int32, (n,))
     elif n > desc.batch:
         raise ValueError(f"{n} tokens without req: row i belongs to request i of {desc.batch}")
     return n
@@ -255,11 +266,12 @@ def _tokens(desc: CacheDesc, req, pos) -> int:
 
 def dcp_kv_gather(desc: CacheDesc, req, pos, k_out, v_out=None, rank=None, stream=None) -> None:
     """Read rows back as bf16: k_out [n][hkv][dk] (MLA [n][576]), v_out alike or None."""
-    n = _tokens(desc, req, pos)
+    device = _device()
+    n = _tokens(desc, req, pos, device)
     shape = (n, desc.hkv, desc.dk) if desc.kind == DCP_GQA else (n, desc.dk)
-    _tensor("k_out", k_out, "bfloat16", shape)
+    _tensor("k_out", k_out, device, _torch.bfloat16, shape)
     if v_out is not None:
-        _tensor("v_out", v_out, "bfloat16", shape)
+        _tensor("v_out", v_out, device, _torch.bfloat16, shape)
     _check(lib().dcp_kv_gather(ctypes.byref(desc), _rank(rank), n, _ptr(req), _ptr(pos), _ptr(k_out), _ptr(v_out),
                                _stream(stream)), "dcp_kv_gather")
 
@@ -283,17 +295,16 @@ def make_rope(rot_dim: int, *, layout: str = "half", theta: float = 1e4, scaling
     return rope
 
 
-def _rows(name: str, t, shape) -> int:
+def _rows(name: str, t, device: int, shape) -> int:
     """Token stride (elements) of rows [n][..] whose inner dimensions are contiguous."""
-    _tensor(name, t, "bfloat16")
-    if tuple(t.shape) != tuple(shape):
+    _tensor(name, t, device, _torch.bfloat16)
+    if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, not {tuple(shape)}")
-    inner = 1
-    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if size > 1 and stride != inner:
-            raise ValueError(f"{name}: a token's row is not contiguous (strides {t.stride()})")
-        inner *= size
-    return t.stride(0) if t.shape[0] > 1 else inner
+    strides = t.stride()
+    row = shape[1] * shape[2] if len(shape) == 3 else shape[1]
+    if strides[-1] != 1 or (len(shape) == 3 and shape[1] > 1 and strides[1] != shape[2]):
+        raise ValueError(f"{name}: a token's row is not contiguous (strides {strides})")
+    return strides[0] if shape[0] > 1 else row
 
 
 def dcp_norm_rope_append(desc: CacheDesc, rope, req, pos, q, k, v, q_weight, k_weight, eps: float, q_out, rank=None,
@@ -303,23 +314,25 @@ def dcp_norm_rope_append(desc: CacheDesc, rope, req, pos, q, k, v, q_weight, k_w
     q bf16 [n][hq][dk], k / v bf16 [n][hkv][dk] (MLA: k [n][576], v None), rows may be strided by token (slices of
     one projection's output); q_weight / k_weight bf16 [dk] (MLA: None and [512]) or None for no norm; rope from
     make_rope or None; q_out bf16 [n][hq][dk], which may be q itself.  q and q_out, or k and v, may be None."""
-    n = _tokens(desc, req, pos)
+    device = _device()
+    n = _tokens(desc, req, pos, device)
     mla = desc.kind == DCP_MLA
+    hq, hkv, dk = desc.hq, desc.hkv, desc.dk
     qs = ks = vs = 0
     if q is not None:
-        qs = _rows("q", q, (n, desc.hq, desc.dk))
+        qs = _rows("q", q, device, (n, hq, dk))
         if q_out is None:
             raise ValueError("q without q_out")
-        _tensor("q_out", q_out, "bfloat16", (n, desc.hq, desc.dk))
-    kv_shape = (n, desc.dk) if mla else (n, desc.hkv, desc.dk)
+        _tensor("q_out", q_out, device, _torch.bfloat16, (n, hq, dk))
+    kv_shape = (n, dk) if mla else (n, hkv, dk)
     if k is not None:
-        ks = _rows("k", k, kv_shape)
+        ks = _rows("k", k, device, kv_shape)
     if v is not None:
-        vs = _rows("v", v, kv_shape)
+        vs = _rows("v", v, device, kv_shape)
     if q_weight is not None:
-        _tensor("q_weight", q_weight, "bfloat16", (desc.dk,))
+        _tensor("q_weight", q_weight, device, _torch.bfloat16, (dk,))
     if k_weight is not None:
-        _tensor("k_weight", k_weight, "bfloat16", (512 if mla else desc.dk,))
+        _tensor("k_weight", k_weight, device, _torch.bfloat16, (512 if mla else dk,))
     _check(lib().dcp_norm_rope_append(ctypes.byref(desc), _rank(rank), None if rope is None else ctypes.byref(rope), n,
                                       _ptr(req), _ptr(pos), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(q_weight),
                                       _ptr(k_weight), eps, _ptr(q_out if q is not None else None), _stream(stream)),
@@ -336,13 +349,15 @@ def dcp_decode_window(desc: CacheDesc, q, seq_lens, window: int, n_sinks: int, o
     """Decode attention under a sliding window of `window` positions and `n_sinks` first tokens.
     q bf16 [B][hq][dk] or [B][q_len][hq][dk]; out / lse fp32 with q's leading dimensions; rank None: all shards
     merged, r: rank r's partial of a multi-GPU group."""
-    lead = tuple(q.shape[:-1])
-    q_len = 1 if q.dim() == 3 else q.shape[1]
-    _tensor("q", q, "bfloat16", lead[:-1] + (desc.hq, desc.dk))
-    _tensor("seq_lens", seq_lens, "int32", (q.shape[0],))
-    _tensor("out", out, "float32", lead + (desc.dv,))
-    _tensor("lse", lse, "float32", lead)
-    _check(lib().dcp_decode_window(ctypes.byref(desc), _rank(rank), q.shape[0], q_len, window, n_sinks, _ptr(q),
+    device, shape, hq = _device(), q.shape, desc.hq
+    B, q_len = shape[0], 1 if len(shape) == 3 else shape[1]
+    lead = (B, hq) if len(shape) == 3 else (B, q_len, hq)
+    f32 = _torch.float32
+    _tensor("q", q, device, _torch.bfloat16, lead + (desc.dk,))
+    _tensor("seq_lens", seq_lens, device, _torch.int32, (B,))
+    _tensor("out", out, device, f32, lead + (desc.dv,))
+    _tensor("lse", lse, device, f32, lead)
+    _check(lib().dcp_decode_window(ctypes.byref(desc), _rank(rank), B, q_len, window, n_sinks, _ptr(q),
                                    _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
                                    _stream(stream)), "dcp_decode_window")
 

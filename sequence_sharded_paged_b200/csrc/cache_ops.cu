@@ -151,9 +151,9 @@ __global__ void append_mla_fp8_kernel(AppendArgs a) {
 // scale of its 16 dimensions.  The token's page is looked up once for up to
 // kHeadsPerLane heads, whose K and V rows are all loaded before any is
 // quantised.  Bound by HBM: 4 D bytes in and 2 (D/2 + D/16) out for each head.
-constexpr int kHeadsPerLane = 4;
+constexpr int kHeadsPerLane = 2;
 
-__global__ void __launch_bounds__(256) append_gqa_fp4_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(256, 6) append_gqa_fp4_kernel(AppendArgs a) {
     const int lpr = a.dk / 8;
     const int hb = (a.hkv + kHeadsPerLane - 1) / kHeadsPerLane;
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
@@ -199,7 +199,7 @@ __device__ __forceinline__ uint4 load_fp4x8(const uint8_t* blk, int P, int D, in
 }
 
 // Read-back, GQA: the append's lanes in reverse (bf16 or 4-bit pools).
-__global__ void __launch_bounds__(256) gather_gqa_kernel(AppendArgs a, uint8_t* k_out, uint8_t* v_out) {
+__global__ void __launch_bounds__(256, 6) gather_gqa_kernel(AppendArgs a, uint8_t* k_out, uint8_t* v_out) {
     const int lpr = a.dk / 8;
     const int hb = (a.hkv + kHeadsPerLane - 1) / kHeadsPerLane;
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;

@@ -67,8 +67,12 @@ struct Lane {
     static constexpr int kV = FP4 ? 4 * D / 16 : 4 * (D / 64) * 16;
     static constexpr int kS = FP4 ? (D / 64 + 1) * 4 : 0;
     static constexpr int kStage = 32 * (kK + kV + kS);
-    // groups in the queue: as many as let three CTAs share an SM
-    static constexpr int kStages = FP4 ? (D == 128 ? 7 : 12) : (D == 128 ? 2 : 4);
+    // Groups that one softmax step takes.  4-bit: two, since the work for each byte is
+    // what bounds it and two groups share the step's votes and hide each other's
+    // latencies; bf16: one, since the bytes in flight are what counts.
+    static constexpr int kStep = FP4 ? 2 : 1;
+    static constexpr int kSteps = FP4 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4);  // steps in the queue
+    static constexpr int kStages = kStep * kSteps;
 };
 
 struct StreamArgs {
@@ -94,17 +98,35 @@ struct StreamArgs {
     int32_t team;     // warps per team: 1 or kWarps
     int32_t workers;  // teams in the grid
     int32_t whole;    // whole segments, else equal shares
+    int32_t lead;     // what a segment costs beside its groups, in groups (shares count it)
     float scale_log2;
 };
 
+// copies of this thread's own bytes; a masked copy that is not live writes zeros
+template <bool MASK>
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+    if (MASK)
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                     "r"(live ? 16 : 0)
+                     : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+template <bool MASK>
 __device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
+    if (MASK)
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+template <bool MASK>
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+    if (MASK)
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -116,14 +138,12 @@ template <bool FP4>
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
     if (FP4)
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
-            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -168,7 +188,8 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
     }
 }
 
-// positions p < x that shard n owns
+// positions p < x that a shard owns; `off` is the shard's first position in a round,
+// n * interleave (saturated, like a.in)
 struct Counter {
     uint32_t base, rest;
     __device__ __forceinline__ Counter(uint32_t x, const StreamArgs& a) {
@@ -176,30 +197,51 @@ struct Counter {
         base = q * (uint32_t)a.interleave;
         rest = x - q * a.in;
     }
-    __device__ __forceinline__ int of(int n, const StreamArgs& a) const {
-        const int64_t r = (int64_t)rest - (int64_t)n * a.interleave;
-        return (int)(base + (uint32_t)(r < 0 ? 0 : r > a.interleave ? a.interleave : r));
+    __device__ __forceinline__ int of(uint32_t off, uint32_t interleave) const {
+        return (int)(base + min(rest - min(rest, off), interleave));
     }
 };
+
+__device__ __forceinline__ uint32_t round_offset(const StreamArgs& a, int n) {
+    const uint64_t off = (uint64_t)(uint32_t)n * (uint32_t)a.interleave;
+    return off > 0xffffffffu ? 0xffffffffu : (uint32_t)off;
+}
 
 // What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
 // when the two meet).
 struct Visible {
     int L, first;  // length, position of query token 0 (may be negative)
+    bool ends;     // sinks and window apart
     Counter cs, cl, ch;
     __device__ __forceinline__ Visible(int len, const StreamArgs& a)
-        : L(len), first(len - a.q_len), cs(0, a), cl(0, a), ch((uint32_t)len, a) {
+        : L(len), first(len - a.q_len), ends(false), cs(0, a), cl(0, a), ch((uint32_t)len, a) {
         const int lo = a.window > first ? 0 : first - a.window + 1;
         if (lo > a.sinks) {
+            ends = true;
             cs = Counter((uint32_t)a.sinks, a);
             cl = Counter((uint32_t)lo, a);
         }
     }
-    // shard n's groups: [0, sg) and [w0, w1)
-    __device__ __forceinline__ void groups(int n, const StreamArgs& a, int* sg, int* w0, int* w1) const {
-        *sg = (cs.of(n, a) + kTok - 1) / kTok;
-        *w0 = max(cl.of(n, a) / kTok, *sg);
-        *w1 = max((ch.of(n, a) + kTok - 1) / kTok, *w0);
+    // groups of the shard at `off`: [0, sg) and [w0, w1)
+    __device__ __forceinline__ void groups(uint32_t off, const StreamArgs& a, int* sg, int* w0, int* w1) const {
+        const uint32_t I = (uint32_t)a.interleave;
+        *w1 = (ch.of(off, I) + kTok - 1) / kTok;
+        *sg = *w0 = 0;
+        if (ends) {
+            *sg = (cs.of(off, I) + kTok - 1) / kTok;
+            *w0 = max(cl.of(off, I) / kTok, *sg);
+            *w1 = max(*w0, *w1);
+        }
+    }
+    // all groups of shards [lo, hi)
+    __device__ __forceinline__ int count(int lo, int hi, const StreamArgs& a) const {
+        int g = 0;
+        for (int n = lo; n < hi; n++) {
+            int sg, w0, w1;
+            groups(round_offset(a, n), a, &sg, &w0, &w1);
+            g += sg + w1 - w0;
+        }
+        return g;
     }
 };
 
@@ -207,22 +249,20 @@ __device__ __forceinline__ int length_of(const StreamArgs& a, int b) { return ma
 
 // groups of base (block of shards, request); at least 1, so that every row is written
 __device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
-    const int blk = base / a.batch;
+    const int blk = a.per_shard ? base / a.batch : 0;
     const Visible v(length_of(a, base - blk * a.batch), a);
-    const int lo = a.per_shard ? a.shard_lo + blk : a.shard_lo, hi = a.per_shard ? lo + 1 : a.shard_hi;
-    int g = 0;
-    for (int n = lo; n < hi; n++) {
-        int sg, w0, w1;
-        v.groups(n, a, &sg, &w0, &w1);
-        g += sg + w1 - w0;
-    }
-    return max(g, 1);
+    const int lo = a.shard_lo + blk, hi = a.per_shard ? lo + 1 : a.shard_hi;
+    return max(v.count(lo, hi, a), 1);
 }
 
-// A group: its page (-1: none), first local token, shard, and whether every row
-// sees all of it.
-struct Desc {
-    int page, t0, shard, full;
+// A group: byte offset of its first row in the pools (bf16) or of its block (4-bit),
+// -1: no page; first local token; shard; whether every row sees all of it.
+struct __align__(16) Desc {
+    int64_t off;
+    int t0;
+    int shard_full;
+    __device__ __forceinline__ int shard() const { return shard_full & 0x7fffffff; }
+    __device__ __forceinline__ bool full() const { return shard_full < 0; }
 };
 
 __device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
@@ -239,20 +279,27 @@ template <bool FP4, int D, bool HALF>
 struct Warp {
     static constexpr int KS = D / 16;  // k-steps of Q K^T
     static constexpr int NT = D / 8;   // n-tiles of P V
+    static constexpr int H = HALF ? 1 : 2;  // rows of this thread: qr (and qr + 8)
     using C = Lane<FP4, D>;
     static constexpr float kBias = FP4 ? 7.f : 0.f;
+    static constexpr uint32_t kOnes = FP4 ? 0x3c003c00u : 0x3f803f80u;
 
     uint32_t q[KS][HALF ? 2 : 4];
     float o[NT][4];
+    float ol[4];  // sum of P by the same instruction: it cuts off what the product cuts off
     float m[2], l[2], scale[2];
     int at[2];  // positions of rows qr and qr + 8
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
         for (int j = 0; j < NT; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        ol[0] = ol[1] = ol[2] = ol[3] = 0.f;
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
+
+    // first of the 8 dimensions that thread column n holds in n-tiles 8 w .. 8 w + 7
+    __device__ __forceinline__ static int dim_of(int n, int w) { return FP4 ? n * NT + 8 * w : (n + 8 * w) * 8; }
 
     // Q fragments of rows qr (and qr + 8) of tile `tile` of KV head g
     __device__ __forceinline__ void load_q(const StreamArgs& a, int b, int g, int tile, int L, float kf) {
@@ -263,7 +310,7 @@ struct Warp {
             const bool live = r < a.rows && !(HALF && h);
             const int j = live ? r / a.group : 0, hh = live ? r - j * a.group : 0;
             at[h] = live ? L - a.q_len + j : INT_MIN / 2;
-            scale[h] = a.scale_log2;
+            scale[h] = fabsf(a.scale_log2);
             if (HALF && h) continue;
             const uint2* src = reinterpret_cast<const uint2*>(
                 a.q + (((int64_t)b * a.q_len + j) * a.hq + g * a.group + hh) * D);  // 4 dimensions each
@@ -272,6 +319,10 @@ struct Warp {
             for (int s = 0; s < KS; s++) {
                 const int d4 = FP4 ? (D / 4 * c) / 4 + s : (s >> 1) * 8 + c * 2 + (s & 1);
                 w[s] = live ? __ldg(src + d4) : make_uint2(0, 0);
+                if (a.scale_log2 < 0.f) {  // the sign of the scale goes into q: scale[] >= 0
+                    w[s].x ^= 0x80008000u;
+                    w[s].y ^= 0x80008000u;
+                }
             }
             if (FP4) {
                 // a power of two brings the row's largest magnitude into [1, 2)
@@ -285,7 +336,7 @@ struct Warp {
                 int e = (int)(__float_as_uint(amax) >> 23) - 127;
                 e = (e > 127 || amax == 0.f) ? 0 : min(126, max(-126, e));
                 const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                scale[h] = a.scale_log2 * kf * __uint_as_float((uint32_t)(127 + e) << 23);
+                scale[h] = fabsf(a.scale_log2) * kf * __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
                 for (int s = 0; s < KS; s++) {
                     const __half2 x = __floats2half2_rn(bf16_lo(w[s].x) * f, bf16_hi(w[s].x) * f);
@@ -307,64 +358,71 @@ struct Warp {
         }
     }
 
-    // Start the copies of group d of KV head g into queue slot `slot`.
-    __device__ __forceinline__ static void issue(const StreamArgs& a, const Desc& d, int g, int L, uint32_t slot) {
-        if (d.page < 0) return;
-        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        const int P = a.page_size, sub = d.t0 & (P - 1);
-        const int64_t blk = (int64_t)d.page * a.hkv + g;
-        const int kt = 4 * (n >> 1) + (n & 1);  // K: token of tile 0 (tile 1: + 2)
-        bool lk[2] = {true, true}, lv[4] = {true, true, true, true};
-        if (!d.full) {  // a token is copied if any query token sees it
-            const int first = L - a.q_len;
-#pragma unroll
-            for (int e = 0; e < 6; e++) {
-                const int64_t p = position_of(a, d.shard, d.t0 + (e < 2 ? kt + 2 * e : 4 * c + e - 2));
-                const bool any = p < L && (p < a.sinks || first - p < a.window);
-                if (e < 2)
-                    lk[e] = any;
-                else
-                    lv[e - 2] = any;
-            }
+    // Start the copies of group d into queue slot `slot`.
+    __device__ __forceinline__ static void issue(const StreamArgs& a, const Desc& d, int L, uint32_t slot) {
+        if (d.off < 0) return;
+        bool live[6] = {true, true, true, true, true, true};  // K tiles' tokens, V's four tokens
+        if (d.full()) {
+            copy<false>(a, d, live, slot);
+            return;
         }
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        const int first = L - a.q_len;
+#pragma unroll
+        for (int e = 0; e < 6; e++) {  // a token is copied if any query token sees it
+            const int64_t p =
+                position_of(a, d.shard(), d.t0 + (e < 2 ? 4 * (n >> 1) + (n & 1) + 2 * e : 4 * c + e - 2));
+            live[e] = p < L && (p < a.sinks || first - p < a.window);
+        }
+        copy<true>(a, d, live, slot);
+    }
+
+    template <bool MASK>
+    __device__ __forceinline__ static void copy(const StreamArgs& a, const Desc& d, const bool* live, uint32_t slot) {
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        const int P = a.page_size;
+        const int kt = 4 * (n >> 1) + (n & 1);  // K: token of tile 0 (tile 1: + 2)
         if (!FP4) {
-            const uint8_t* kb = a.k_pages + (blk * P + sub) * (D * 2) + kt * (D * 2) + c * 16;
-            const uint8_t* vb = a.v_pages + (blk * P + sub) * (D * 2) + 4 * c * (D * 2) + n * (D / 4);
+            const uint8_t* kb = a.k_pages + d.off + (kt * (D * 2) + c * 16);
+            const uint8_t* vb = a.v_pages + d.off + (4 * c * (D * 2) + n * 16);
             const uint32_t dst = slot + lane * 16;
 #pragma unroll
             for (int t = 0; t < 2; t++)
 #pragma unroll
                 for (int i = 0; i < D / 32; i++)
-                    cp16(dst + (t * (D / 32) + i) * 512, kb + t * 2 * (D * 2) + i * 64, lk[t]);
+                    cp16<MASK>(dst + (t * (D / 32) + i) * 512, kb + t * 2 * (D * 2) + i * 64, live[t]);
 #pragma unroll
             for (int e = 0; e < 4; e++)
 #pragma unroll
                 for (int i = 0; i < D / 64; i++)
-                    cp16(dst + C::kK * 32 + (e * (D / 64) + i) * 512, vb + e * (D * 2) + i * 16, lv[e]);
+                    cp16<MASK>(dst + C::kK * 32 + (e * (D / 64) + i) * 512, vb + e * (D * 2) + i * 128, live[2 + e]);
         } else {
-            const int64_t off = blk * fp4_block_bytes(P, D);
-            const uint8_t* kb = a.k_pages + off + (sub + kt) * (D / 2) + c * (D / 8);
-            const uint8_t* vb = a.v_pages + off + (sub + 4 * c) * (D / 2) + n * (D / 16);
-            const uint8_t* ks = a.k_pages + off + P * (D / 2) + (c * (D / 64)) * P + sub + 4 * (n >> 1);
-            const uint8_t* vs = a.v_pages + off + P * (D / 2) + (n * D / 128) * P + sub + 4 * c;
+            const int sub = d.t0 & (P - 1);
+            const uint8_t* kb = a.k_pages + d.off;
+            const uint8_t* vb = a.v_pages + d.off;
+            const int kc = (sub + kt) * (D / 2) + c * (D / 8), vc = (sub + 4 * c) * (D / 2) + n * (D / 16);
             // scale words hold four tokens; a token that is not copied has zero codes
+            const int ks = P * (D / 2) + (c * (D / 64)) * P + sub + 4 * (n >> 1);
+            const int vs = P * (D / 2) + (n * D / 128) * P + sub + 4 * c;
             const uint32_t ds = slot + (C::kK + C::kV) * 32 + lane * 4;
             if (D == 128) {
-                cp16(slot + lane * 16, kb, lk[0]);
-                cp16(slot + 512 + lane * 16, kb + 2 * (D / 2), lk[1]);
+                cp16<MASK>(slot + lane * 16, kb + kc, live[0]);
+                cp16<MASK>(slot + 512 + lane * 16, kb + kc + 2 * (D / 2), live[1]);
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    cp8(slot + 1024 + (e >> 1) * 512 + lane * 16 + (e & 1) * 8, vb + e * (D / 2), lv[e]);
-                cp4(ds, ks, true);
-                cp4(ds + 128, ks + P, true);
-                cp4(ds + 256, vs, true);
+                    cp8<MASK>(slot + 1024 + (e >> 1) * 512 + lane * 16 + (e & 1) * 8, vb + vc + e * (D / 2),
+                              live[2 + e]);
+                cp4<false>(ds, kb + ks, true);
+                cp4<false>(ds + 128, kb + ks + P, true);
+                cp4<false>(ds + 256, vb + vs, true);
             } else {
-                cp8(slot + lane * 16, kb, lk[0]);
-                cp8(slot + lane * 16 + 8, kb + 2 * (D / 2), lk[1]);
+                cp8<MASK>(slot + lane * 16, kb + kc, live[0]);
+                cp8<MASK>(slot + lane * 16 + 8, kb + kc + 2 * (D / 2), live[1]);
 #pragma unroll
-                for (int e = 0; e < 4; e++) cp4(slot + 512 + lane * 16 + e * 4, vb + e * (D / 2), lv[e]);
-                cp4(ds, ks, true);
-                cp4(ds + 128, vs, true);
+                for (int e = 0; e < 4; e++)
+                    cp4<MASK>(slot + 512 + lane * 16 + e * 4, vb + vc + e * (D / 2), live[2 + e]);
+                cp4<false>(ds, kb + ks, true);
+                cp4<false>(ds + 128, vb + vs, true);
             }
         }
     }
@@ -413,10 +471,9 @@ struct Warp {
         }
     }
 
-    // One group: scores, softmax step, O += P V.
-    __device__ __forceinline__ void consume(const StreamArgs& a, const Desc& d, const uint8_t* slot) {
-        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        float x[2][4];
+    // Scores of one group: x[t][e], e = 0, 1: row qr, token 4c + 2t + e; e = 2, 3: row qr + 8
+    __device__ __forceinline__ void scores(const uint8_t* slot, float (*x)[4]) {
+        const int lane = threadIdx.x & 31, n = lane >> 2;
 #pragma unroll
         for (int t = 0; t < 2; t++) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
         if (!FP4) {
@@ -453,29 +510,39 @@ struct Warp {
                 }
             }
         }
-        bool vis[2][4];  // [row][token 4c + e]
-        if (!d.full) {
+    }
+
+    // G groups (slots slot[0 .. G-1]): scores, one softmax step, O += P V.  MASK: one
+    // group that not every row sees all of.
+    template <int G, bool MASK>
+    __device__ __forceinline__ void consume(const StreamArgs& a, const Desc& d, const uint8_t* const* slot) {
+        const int c = threadIdx.x & 3;
+        float x[2 * G][4];
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const int64_t p = position_of(a, d.shard, d.t0 + 4 * c + e);
-                vis[0][e] = sees(a, p, at[0]);
-                vis[1][e] = sees(a, p, at[1]);
+        for (int g = 0; g < G; g++) scores(slot[g], x + 2 * g);
+        if (MASK) {
+#pragma unroll
+            for (int e = 0; e < 4; e++) {  // token 4c + e
+                const int64_t p = position_of(a, d.shard(), d.t0 + 4 * c + e);
+#pragma unroll
+                for (int h = 0; h < H; h++)
+                    if (!sees(a, p, at[h])) x[e >> 1][2 * h + (e & 1)] = -INFINITY;
             }
         }
-        // x[t][e], e = 0, 1: row qr, token 4c + 2t + e; e = 2, 3: row qr + 8
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[H];
+        bool grow = false;
 #pragma unroll
-        for (int t = 0; t < 2; t++)
+        for (int h = 0; h < H; h++) {
+            mx[h] = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < (HALF ? 2 : 4); e++) {
-                x[t][e] *= scale[e >> 1];
-                if (!d.full && !vis[e >> 1][2 * t + (e & 1)]) x[t][e] = -INFINITY;
-                mx[e >> 1] = fmaxf(mx[e >> 1], x[t][e]);
-            }
-        const bool grow = mx[0] > m[0] + (kLazy + kBias) || (!HALF && mx[1] > m[1] + (kLazy + kBias));
+            for (int t = 0; t < 2 * G; t++) mx[h] = fmaxf(mx[h], fmaxf(x[t][2 * h], x[t][2 * h + 1]));
+            // scale = 0 (a query of zeros has scale > 0; the caller's scale may be 0): 0 * -inf stays masked
+            mx[h] = mx[h] == -INFINITY ? -INFINITY : mx[h] * scale[h];
+            grow |= mx[h] > m[h] + (kLazy + kBias);
+        }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-            for (int h = 0; h < (HALF ? 1 : 2); h++) {
+            for (int h = 0; h < H; h++) {
                 float t = mx[h];
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
@@ -484,46 +551,74 @@ struct Warp {
                     const float f = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
                     m[h] = mn;
                     l[h] *= f;
-#pragma unroll
-                    for (int j = 0; j < NT; j++) {
-                        o[j][2 * h] *= f;
-                        o[j][2 * h + 1] *= f;
-                        if (HALF) {
-                            o[j][2] *= f;
-                            o[j][3] *= f;
-                        }
-                    }
+                    rescale(h, f);
                 }
             }
         }
-        uint32_t hi[4], lo[4];  // A operands: [row half + 2 * tile]
+        uint32_t hi[G][4], lo[G][4];  // A operands: [row half + 2 * tile]
 #pragma unroll
-        for (int h = 0; h < (HALF ? 1 : 2); h++) {
+        for (int h = 0; h < H; h++) {
             const float ref = m[h] == -INFINITY ? 0.f : m[h];
+            float sum = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
-                const float p0 = fast_exp2(x[t][2 * h] - ref), p1 = fast_exp2(x[t][2 * h + 1] - ref);
-                l[h] += p0 + p1;
-                split2<FP4>(p0, p1, hi[h + 2 * t], lo[h + 2 * t]);
+            for (int t = 0; t < 2 * G; t++) {
+                float p[2];
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    p[e] = fast_exp2(fmaf(x[t][2 * h + e], scale[h], -ref));
+                    if (MASK && x[t][2 * h + e] == -INFINITY) p[e] = 0.f;  // also where the scale is 0
+                }
+                sum += p[0] + p[1];
+                split2<FP4>(p[0], p[1], hi[t >> 1][h + 2 * (t & 1)], lo[t >> 1][h + 2 * (t & 1)]);
             }
+            l[h] += sum;
         }
         if (HALF) {  // rows 8..15 carry the low terms
-            hi[1] = lo[0];
-            hi[3] = lo[2];
+#pragma unroll
+            for (int g = 0; g < G; g++) {
+                hi[g][1] = lo[g][0];
+                hi[g][3] = lo[g][2];
+            }
         }
-        if (!d.full && a.q_len > 1 && poisoned(slot)) {
-            careful(a, d, slot, hi, lo, vis);
+        if (MASK && a.q_len > 1 && poisoned(slot[0])) {
+            careful(a, d, slot[0], hi[0], lo[0]);
             return;
         }
 #pragma unroll
-        for (int w = 0; w < NT / 8; w++) {
-            uint32_t b[8][2];
-            load_v(slot, w, b);
+        for (int g = 0; g < G; g++) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) {
-                mma<FP4>(o[8 * w + j], hi[0], hi[1], hi[2], hi[3], b[j][0], b[j][1]);
-                if (!HALF) mma<FP4>(o[8 * w + j], lo[0], lo[1], lo[2], lo[3], b[j][0], b[j][1]);
+            for (int w = 0; w < NT / 8; w++) {
+                uint32_t b[8][2];
+                load_v(slot[g], w, b);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    mma<FP4>(o[8 * w + j], hi[g][0], hi[g][1], hi[g][2], hi[g][3], b[j][0], b[j][1]);
+                if (!HALF) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        mma<FP4>(o[8 * w + j], lo[g][0], lo[g][1], lo[g][2], lo[g][3], b[j][0], b[j][1]);
+                }
             }
+            mma<FP4>(ol, hi[g][0], hi[g][1], hi[g][2], hi[g][3], kOnes, kOnes);
+            if (!HALF) mma<FP4>(ol, lo[g][0], lo[g][1], lo[g][2], lo[g][3], kOnes, kOnes);
+        }
+    }
+
+    __device__ __forceinline__ void rescale(int h, float f) {
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+            o[j][2 * h] *= f;
+            o[j][2 * h + 1] *= f;
+            if (HALF) {
+                o[j][2] *= f;
+                o[j][3] *= f;
+            }
+        }
+        ol[2 * h] *= f;
+        ol[2 * h + 1] *= f;
+        if (HALF) {
+            ol[2] *= f;
+            ol[3] *= f;
         }
     }
 
@@ -553,8 +648,8 @@ struct Warp {
 
     // P V where some rows must not see a non-finite value that others see: row by
     // row, with the values that the row does not see set to zero.
-    __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot, const uint32_t* hi,
-                                         const uint32_t* lo, bool (*vis)[4]) {
+    __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot,
+                                            const uint32_t* hi, const uint32_t* lo) {
         const int lane = threadIdx.x & 31, qr = lane >> 2;
 #pragma unroll 1
         for (int r = 0; r < (HALF ? 8 : 16); r++) {
@@ -566,7 +661,7 @@ struct Warp {
                 keep[h] = 0;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int64_t p = position_of(a, d.shard, d.t0 + 4 * (lane & 3) + 2 * h + e);
+                    const int64_t p = position_of(a, d.shard(), d.t0 + 4 * (lane & 3) + 2 * h + e);
                     if (sees(a, p, at_r)) keep[h] |= 0xffffu << (16 * e);
                 }
             }
@@ -587,6 +682,8 @@ struct Warp {
                 }
             }
         }
+        mma<FP4>(ol, hi[0], hi[1], hi[2], hi[3], kOnes, kOnes);
+        if (!HALF) mma<FP4>(ol, lo[0], lo[1], lo[2], lo[3], kOnes, kOnes);
     }
 
     // After the last group: whole-row sums, the low terms folded in, l and m the same
@@ -603,6 +700,7 @@ struct Warp {
                 o[j][0] += o[j][2];
                 o[j][1] += o[j][3];
             }
+            ol[0] += ol[2];
         }
     }
 };
@@ -632,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
     static_assert(kRing >= kRows * kPitch * 4, "a warp's queue holds its O");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Desc s_desc[kWarps][kDescs];
-    __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+    __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_ol[kWarps][16];
     __shared__ long long s_scan[kWarps];
     __shared__ int s_base[kWarps], s_off[kWarps];  // per team: where its share begins
     __shared__ int s_sub[kWarps];
@@ -657,13 +755,18 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
     // this worker's share: segments [seg, ..) step `workers`, or flat groups [r0, r1)
     long long r0 = 0, r1 = 0, total = 0;
     int active = a.workers;
-    int base = 0, sub = 0, i0 = 0;
+    int base = 0, sub = 0, x0 = 0;  // x0: where in the segment (its lead, then its groups)
     if (!a.whole) {
         // every CTA sums all bases' groups, a run of consecutive bases for each thread
         const int each = (nb + kThreads - 1) / kThreads;
         const int b0 = min(nb, (int)threadIdx.x * each), b1 = min(nb, b0 + each);
         long long mine = 0;
-        for (int b = b0; b < b1; b++) mine += (long long)base_groups(a, b) * per_base;
+        int first_groups = 0;  // of base b0
+        for (int b = b0; b < b1; b++) {
+            const int g = base_groups(a, b);
+            if (b == b0) first_groups = g;
+            mine += (long long)(g + a.lead) * per_base;
+        }
         long long incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -685,12 +788,12 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
             long long at = total * w / active - (incl - mine);
             if (at < 0 || at >= mine) continue;
             for (int b = b0; b < b1; b++) {
-                const int g = base_groups(a, b);
-                const long long size = (long long)g * per_base;
+                const int g = b == b0 ? first_groups : base_groups(a, b);
+                const long long size = (long long)(g + a.lead) * per_base;
                 if (at < size) {
                     s_base[t] = b;
-                    s_sub[t] = (int)(at / g);
-                    s_off[t] = (int)(at % g);
+                    s_sub[t] = (int)(at / (g + a.lead));
+                    s_off[t] = (int)(at % (g + a.lead));
                     break;
                 }
                 at -= size;
@@ -702,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
             r1 = total * (worker + 1) / active;
             base = s_base[team];
             sub = s_sub[team];
-            i0 = s_off[team];
+            x0 = s_off[team];
         }
     }
     int4 tail = make_int4(-1, 0, 0, 0);
@@ -717,54 +820,53 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
             __syncthreads();
     };
 
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     while (a.whole ? seg < (long long)nb * per_base : pos < r1) {
         if (a.whole) {
             base = (int)(seg / per_base);
             sub = (int)(seg - (long long)base * per_base);
-            i0 = 0;
         }
-        const int blk = base / a.batch, b = base - blk * a.batch;
+        const int blk = a.per_shard ? base / a.batch : 0, b = base - blk * a.batch;
         const int g = sub / a.tiles, tile = sub - g * a.tiles;
-        const int lo = a.per_shard ? a.shard_lo + blk : a.shard_lo, hi = a.per_shard ? lo + 1 : a.shard_hi;
+        const int lo = a.shard_lo + blk, hi = a.per_shard ? lo + 1 : a.shard_hi;
         const int L = length_of(a, b);
         const Visible v(L, a);
-        int ng = 0;
-        for (int n = lo; n < hi; n++) {
-            int sg, w0, w1;
-            v.groups(n, a, &sg, &w0, &w1);
-            ng += sg + w1 - w0;
-        }
-        const int real = ng;  // 0: nothing visible, one empty group
-        ng = max(ng, 1);
-        const int take = a.whole ? ng : (int)min((long long)(ng - i0), r1 - pos);
+        const int real = v.count(lo, hi, a);  // 0: nothing visible, one empty group
+        const int ng = max(real, 1);
+        // groups [i0, i0 + take) of the segment fall to this worker
+        const int x1 = a.whole ? ng : (int)min((long long)(ng + a.lead), x0 + (r1 - pos));
+        const int i0 = a.whole ? 0 : max(0, x0 - a.lead), take = a.whole ? ng : max(0, x1 - a.lead) - i0;
+        if (take > 0) {
         const int nk = wt < take ? (take - wt + a.team - 1) / a.team : 0;  // this warp's groups
 
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
             const int k = 32 * kb + lane;
-            Desc d{-1, 0, 0, 0};
+            Desc d{-1, 0, 0};
             int i = i0 + wt + a.team * k;
             if (k < nk && i < real) {
-                for (int n = lo; n < hi; n++) {
+                int n = lo;
+                for (; n < hi; n++) {
                     int sg, w0, w1;
-                    v.groups(n, a, &sg, &w0, &w1);
+                    v.groups(round_offset(a, n), a, &sg, &w0, &w1);
                     if (i < sg + w1 - w0) {
-                        d.shard = n;
                         d.t0 = kTok * (i < sg ? i : w0 + i - sg);
                         break;
                     }
                     i -= sg + w1 - w0;
                 }
-                const int j = d.t0 / a.page_size;
+                const int P = a.page_size, j = d.t0 / P;
                 int pg = -1;
                 if (j < a.max_local_pages)
-                    pg = __ldg(a.block_tables + ((int64_t)(d.shard - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
+                    pg = __ldg(a.block_tables + ((int64_t)(n - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
                 if (pg < 0 || pg >= a.num_pages)
                     record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
                 else
-                    d.page = pg;
-                const int64_t p0 = position_of(a, d.shard, d.t0), p1 = position_of(a, d.shard, d.t0 + kTok - 1);
-                d.full = p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p0 < a.window);
+                    d.off = ((int64_t)pg * a.hkv + g) * (FP4 ? fp4_block_bytes(P, D) : P * D * 2) +
+                            (FP4 ? 0 : (d.t0 & (P - 1)) * D * 2);
+                const int64_t p0 = position_of(a, n, d.t0), p1 = position_of(a, n, d.t0 + kTok - 1);
+                const bool full = pg >= 0 && p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p0 < a.window);
+                d.shard_full = n | (full && d.off >= 0 ? 0x80000000 : 0);
             }
             __syncwarp();
             descs[(kb & 1) * 32 + lane] = d;
@@ -772,26 +874,46 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
         };
 
         if (nk > 0) batch(0);
+        auto start = [&](int k, int slot) {  // copies of one step, as one commit group
 #pragma unroll
-        for (int k = 0; k < S - 1; k++) {
-            if (k < nk) W::issue(a, descs[k], g, L, ring_u32 + k * C::kStage);
+            for (int e = 0; e < C::kStep; e++)
+                if (k + e < nk) {
+                    if (k + e > 0 && ((k + e) & 31) == 0) batch((k + e) >> 5);
+                    W::issue(a, descs[(k + e) & (kDescs - 1)], L, ring_u32 + (slot + e) * C::kStage);
+                }
             cp_commit();
-        }
+        };
+#pragma unroll
+        for (int k = 0; k < C::kSteps - 1; k++) start(k * C::kStep, k * C::kStep);
         st.reset();
         st.load_q(a, b, g, tile, L, kf);
-        int slot_in = S - 1, slot_out = 0;
-        for (int k = 0; k < nk; k++) {
-            const int f = k + S - 1;
-            if (f < nk) {
-                if ((f & 31) == 0) batch(f >> 5);
-                W::issue(a, descs[f & (kDescs - 1)], g, L, ring_u32 + slot_in * C::kStage);
+        int slot_in = (C::kSteps - 1) * C::kStep, slot_out = 0;
+        for (int k = 0; k < nk; k += C::kStep) {
+            start(k + (C::kSteps - 1) * C::kStep, slot_in);
+            if ((slot_in += C::kStep) == S) slot_in = 0;
+            cp_wait<C::kSteps - 1>();
+            const uint8_t* at = ring + slot_out * C::kStage;
+            if ((slot_out += C::kStep) == S) slot_out = 0;
+            const Desc d0 = descs[k & (kDescs - 1)];
+            if (C::kStep == 1) {
+                if (d0.full())
+                    st.template consume<1, false>(a, d0, &at);
+                else if (d0.off >= 0)
+                    st.template consume<1, true>(a, d0, &at);
+            } else {
+                const uint8_t* two[2] = {at, at + C::kStage};
+                const Desc d1 = descs[(k + 1) & (kDescs - 1)];
+                if (k + 1 < nk && d0.full() && d1.full()) {
+                    st.template consume<2, false>(a, d0, two);
+                } else {
+#pragma unroll 1
+                    for (int e = 0; e < 2 && k + e < nk; e++) {
+                        const Desc d = descs[(k + e) & (kDescs - 1)];
+                        const uint8_t* one = at + e * C::kStage;
+                        if (d.off >= 0) st.template consume<1, true>(a, d, &one);
+                    }
+                }
             }
-            cp_commit();
-            if (++slot_in == S) slot_in = 0;
-            cp_wait<S - 1>();
-            const Desc d = descs[k & (kDescs - 1)];
-            if (d.page >= 0) st.consume(a, d, ring + slot_out * C::kStage);
-            if (++slot_out == S) slot_out = 0;
         }
         cp_wait<0>();
         __syncwarp();  // the next segment's descriptors overwrite these
@@ -818,12 +940,12 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
             for (int h = 0; h < (HALF ? 1 : 2); h++) {
                 const int r = qr + 8 * h;
                 if (r < rows) {
-                    const float inv = st.l[h] == 0.f ? 0.f : vf / st.l[h];
+                    const float inv = st.l[h] == 0.f ? 0.f : vf / st.ol[2 * h];
 #pragma unroll
                     for (int e = 0; e < 2; e++)
 #pragma unroll
                         for (int j = 0; j < W::NT; j += 4)
-                            put(r, (2 * c + e) * W::NT + j,
+                            put(r, W::dim_of(2 * c + e, j / 8) + (j & 7),
                                 make_float4(st.o[j][2 * h + e] * inv, st.o[j + 1][2 * h + e] * inv,
                                             st.o[j + 2][2 * h + e] * inv, st.o[j + 3][2 * h + e] * inv));
                     if (c == 0) put_lse(r, st.l[h] == 0.f ? -INFINITY : (st.m[h] == -INFINITY ? 0.f : st.m[h]) + log2f(st.l[h]));
@@ -840,18 +962,19 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
                 for (int e = 0; e < 2; e++)
 #pragma unroll
                     for (int j = 0; j < W::NT; j += 4)
-                        *reinterpret_cast<float4*>(so + r * kPitch + (2 * c + e) * W::NT + j) =
+                        *reinterpret_cast<float4*>(so + r * kPitch + W::dim_of(2 * c + e, j / 8) + (j & 7)) =
                             make_float4(st.o[j][2 * h + e], st.o[j + 1][2 * h + e], st.o[j + 2][2 * h + e],
                                         st.o[j + 3][2 * h + e]);
                 if (c == 0) {
                     s_m[warp][r] = st.m[h];
                     s_l[warp][r] = st.l[h];
+                    s_ol[warp][r] = st.ol[2 * h];
                 }
             }
             __syncthreads();
             for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
                 const int r = k / (D / 4), d = (k - r * (D / 4)) * 4;
-                float M = -INFINITY, ls = 0.f;
+                float M = -INFINITY, ls = 0.f, ols = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][r]);
                 const float ref = M == -INFINITY ? 0.f : M;
@@ -863,17 +986,18 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
                     const float4 x = *reinterpret_cast<const float4*>(
                         reinterpret_cast<const float*>(smem + (size_t)w * kRing) + r * kPitch + d);
                     ls = fmaf(f, s_l[w][r], ls);
+                    ols = fmaf(f, s_ol[w][r], ols);
                     acc.x = fmaf(f, x.x, acc.x);
                     acc.y = fmaf(f, x.y, acc.y);
                     acc.z = fmaf(f, x.z, acc.z);
                     acc.w = fmaf(f, x.w, acc.w);
                 }
-                const float inv = ls == 0.f ? 0.f : vf / ls;
+                const float inv = ls == 0.f ? 0.f : vf / ols;
                 put(r, d, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
                 if (d == 0) put_lse(r, ls == 0.f ? -INFINITY : ref + log2f(ls));
             }
         }
-        if (a.finish_ns) {
+        if (a.finish_ns && take > 0) {
             team_sync();
             if (wt == 0 && lane == 0) {
                 const uint64_t dt = global_timer_ns() - (uint64_t)*a.t_start;
@@ -882,15 +1006,16 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
         }
         if (!a.whole && starts && !ends) {
             // the worker whose share holds the segment's last group
-            const long long e = pos + ng;  // one past it
+            const long long e = pos - x0 + a.lead + ng;  // one past it
             tail = make_int4(base, sub, (int)((e * active + total - 1) / total) - 1, 0);
         }
         team_sync();  // queues and s_m are free again
+        }
         if (a.whole) {
             seg += a.workers;
         } else {
-            pos += take;
-            i0 = 0;
+            pos += x1 - x0;
+            x0 = 0;
             if (++sub == per_base) {
                 sub = 0;
                 base++;
@@ -903,6 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
 // Sum of a segment's parts: worker w's tail and the heads of the workers after it up
 // to tail[w].z.  CTA (w, block of rows); `wpr` warps share a row's parts.
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ StreamArgs a, int D, int wpr) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete and visible
     const int4 t = a.tail[blockIdx.x];
     if (t.x < 0) return;
     __shared__ float s_w[8];
@@ -996,7 +1122,7 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
     const int64_t warps = (int64_t)num_sms * kCtasPerSm * kWarps, ctas = (int64_t)num_sms * kCtasPerSm;
     const int64_t one = (segs + warps - 1) / warps * groups;
     const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
-    const int64_t share = (segs * groups + warps - 1) / warps + 40;
+    const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
     p.team = 1;
     p.whole = 1;
     int64_t best = one;
@@ -1008,10 +1134,12 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         p.whole = 0;
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
+    p.lead = p.team == 1 ? 2 : 8;
     int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
     if (grid > ctas) grid = ctas;
     p.ctas = (int)grid;
     p.workers = p.ctas * (kWarps / p.team);
+    p.segs = segs;
     p.off_start = 0;
     p.off_tail = 256;
     size_t o = p.off_tail;
@@ -1069,6 +1197,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     a.team = p.team;
     a.workers = p.workers;
     a.whole = p.whole;
+    a.lead = p.lead;
     a.scale_log2 = c->scale * kLog2e;
     if (finish_ns) {
         finish_init_kernel<<<1, 256, 0, s>>>(finish_ns, reinterpret_cast<int64_t*>(w + p.off_start), c->batch);
@@ -1089,11 +1218,19 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
             e = half ? run<false, 128, true>(a, p.ctas, s) : run<false, 128, false>(a, p.ctas, s);
     }
     if (e != cudaSuccess || p.whole) return e;
-    // few teams a segment: a row for each warp; many: a CTA for each row
-    const int wpr = p.team == 1 ? 1 : 8;
+    // few parts a segment: a row for each warp; many: a CTA for each row
+    const int wpr = p.workers >= 8 * p.segs ? 8 : 1;
     const int rows = a.rows < 16 ? a.rows : 16;
-    combine_kernel<<<dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr))), 256, 0, s>>>(a, c->dk, wpr);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;  // the launch overlaps the kernel before it; combine_kernel waits for its end
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, combine_kernel, a, (int)c->dk, wpr);
 }
 
 }  // namespace dcp

@@ -74,7 +74,9 @@ cudaError_t launch_decode_mla_fp8(const DecodeGeometry& g, const DecodeArgs& a, 
 // warp-streamed GQA decode (4-bit caches; sliding window with sinks)
 struct StreamPlan {
     int team, whole;  // warps per team; whole segments or equal shares of all groups
+    int lead;         // a segment's fixed cost, in groups
     int ctas, workers;
+    int64_t segs;
     size_t off_start, off_tail, off_lse, off_o, total;  // workspace
 };
 bool gqa_stream_supported(int hq, int hkv, int dk, int q_len);

@@ -112,11 +112,21 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
     const uint32_t mask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u)) << base_lane;
     const int nq = n.q ? n.hq : 0, nk = a.k_new ? a.hkv : 0;
     const int rows = nq + 2 * nk;  // queries, keys, values of one token
-    const int total = nt * rows;
 
-    auto load = [&](int r) -> uint4 {
-        const int t = r / rows, h = r - t * rows;
-        const int64_t i = i0 + t;
+    // rows are numbered token by token; a group steps GROUPS rows at a time
+    struct At {
+        int t, h;
+    };
+    auto next = [&](At& p) {
+        p.h += GROUPS;
+        while (p.h >= rows) {
+            p.h -= rows;
+            p.t++;
+        }
+    };
+    auto load = [&](const At& p) -> uint4 {
+        const int h = p.h;
+        const int64_t i = i0 + p.t;
         const uint8_t* src = h < nq ? n.q + (i * n.q_stride + (int64_t)h * D) * 2
                              : h < nq + nk ? a.k_new + (i * n.k_stride + (int64_t)(h - nq) * D) * 2
                                            : a.v_new + (i * n.v_stride + (int64_t)(h - nq - nk) * D) * 2;
@@ -124,8 +134,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
     };
     // the first rows' loads overlap the positions', tables' and angles' work
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    if (grp < total) w0 = load(grp);
-    if (grp + GROUPS < total) w1 = load(grp + GROUPS);
+    At p0{0, grp - GROUPS}, p1;
+    next(p0);
+    p1 = p0;
+    next(p1);
+    if (p0.t < nt) w0 = load(p0);
+    if (p1.t < nt) w1 = load(p1);
     uint4 qw = w0, kw = w0;
     if (n.q_weight) qw = __ldg(reinterpret_cast<const uint4*>(n.q_weight) + li);
     if (n.k_weight) kw = __ldg(reinterpret_cast<const uint4*>(n.k_weight) + li);
@@ -144,8 +158,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
     __syncthreads();
     const float fk = a.kv_scales && nk ? __ldg(a.kv_scales) : 1.f, fv = a.kv_scales && nk ? __ldg(a.kv_scales + 1) : 1.f;
 
-    auto process = [&](int r, const uint4& w) {
-        const int t = r / rows, h = r - t * rows;
+    auto process = [&](const At& p, const uint4& w) {
+        const int t = p.t, h = p.h;
         const Target tg = s_target[t];
         if (h >= nq + nk) {
             if (tg.pg >= 0) store_gqa8(a, a.v_pages, tg.pg, h - nq - nk, tg.off, li, w, fv, mask, true);
@@ -163,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
                 for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
                 for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                const float inv = 1.f / sqrtf(ss * (1.f / D) + n.eps);
+                const float inv = rsqrtf(ss * (1.f / D) + n.eps);
                 float wt[8];
                 unpack8(is_q ? qw : kw, wt);
 #pragma unroll
@@ -179,12 +193,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
             store_gqa8(a, a.k_pages, tg.pg, h - nq, tg.off, li, y, fk, mask, true);
         }
     };
-    for (int r = grp; r < total; r += 2 * GROUPS) {
+    while (p0.t < nt) {
         const uint4 c0 = w0, c1 = w1;
-        if (r + 2 * GROUPS < total) w0 = load(r + 2 * GROUPS);
-        if (r + 3 * GROUPS < total) w1 = load(r + 3 * GROUPS);
-        process(r, c0);
-        if (r + GROUPS < total) process(r + GROUPS, c1);
+        const At a0 = p0, a1 = p1;
+        next(p0), next(p0);
+        next(p1), next(p1);
+        if (p0.t < nt) w0 = load(p0);
+        if (p1.t < nt) w1 = load(p1);
+        process(a0, c0);
+        if (a1.t < nt) process(a1, c1);
     }
 }
 
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) norm_rope_mla_kernel(const NormRopeA
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = 1.f / sqrtf(ss * (1.f / NOPE) + n.eps);
+        const float inv = rsqrtf(ss * (1.f / NOPE) + n.eps);
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             float wt[8];
@@ -321,12 +338,9 @@ cudaError_t launch_norm_rope_append(const AppendArgs& a, const dcp_rope* rope, c
         norm_rope_mla_kernel<<<grid, kThreads, 0, s>>>(n, r);
         return cudaGetLastError();
     }
-    // tokens per CTA: enough rows for two rounds of the CTA's groups, as long as
-    // four CTAs for each SM remain
-    const int rows = (q ? hq : 0) + (a.k_new ? 2 * a.hkv : 0);
-    const int groups = kThreads / (a.dk / 8);
-    while (n.tokens < kMaxTokens && n.tokens * rows < 2 * groups && a.n_tok / (2 * n.tokens) >= 4 * num_sms)
-        n.tokens *= 2;
+    // tokens per CTA: what comes before a CTA's first row (positions, tables, angles)
+    // is shared by all its tokens, as long as eight CTAs for each SM remain
+    while (n.tokens < kMaxTokens && a.n_tok / (2 * n.tokens) >= 8 * num_sms) n.tokens *= 2;
     const int64_t blocks = (a.n_tok + n.tokens - 1) / n.tokens;
     if (a.dk == 64)
         norm_rope_gqa_kernel<64><<<(unsigned)blocks, kThreads, 0, s>>>(n, r);

@@ -40,32 +40,56 @@ __device__ __forceinline__ int append_target(const AppendArgs& a, int64_t i, int
     return pg;
 }
 
-// Quantise a run of 16 values held by two neighbouring lanes, 8 each: returns
-// this lane's 8 codes and the run's e4m3 scale byte.  factor > 0 multiplies
-// every scale.  `both` is the mask of the lanes that take part (whole pairs).
-// The scale is rounded up or down to e4m3 first and the codes are taken against
-// the rounded scale, so an element may lie past 6 and saturates there.
-__device__ __forceinline__ uint32_t fp4_quantise8(const float* x, float factor, uint32_t both, uint8_t* scale_byte) {
-    float amax = 0.f;
-    bool nan = false;
+__device__ __forceinline__ uint32_t max2_nan(uint32_t a, uint32_t b) {  // bf16x2, a NaN wins
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                         *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        amax = fmaxf(amax, fabsf(x[e]));
-        nan |= x[e] != x[e];
+    for (int e = 0; e < 4; e++) {
+        x[2 * e] = bf16_lo(ws[e]);
+        x[2 * e + 1] = bf16_hi(ws[e]);
     }
-    float am = nan ? __int_as_float(0x7fc00000) : amax;
-    const float other = __shfl_xor_sync(both, am, 1);
-    am = (am != am || other != other) ? __int_as_float(0x7fc00000) : fmaxf(am, other);
-    const uint8_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(am, 6.f * factor), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Quantise a run of 16 bf16 values held by two neighbouring lanes, 8 each: returns
+// this lane's 8 codes and the run's e4m3 scale byte.  factor > 0 multiplies every
+// scale.  `both` is the mask of the lanes that take part (whole pairs).  The codes
+// are taken against the scale as rounded, so an element may lie past 6 and
+// saturates there.
+//
+// x / s without a division, for factor 1: x has 8 significant bits and a border
+// between two codes, times s, at most 7, so that x / s either IS the border or is
+// 2^-15 away from it, relatively.  x * (1 / s) is within 2^-22; rounding it to 18
+// bits puts it back on the border exactly when x / s is there, and the conversion
+// then takes the even code.
+__device__ __forceinline__ uint32_t fp4_quantise8(const uint4& v, float factor, uint32_t both, uint8_t* scale_byte) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    uint32_t am2 = max2_nan(max2_nan(v.x & kAbs, v.y & kAbs), max2_nan(v.z & kAbs, v.w & kAbs));
+    am2 = max2_nan(am2, __shfl_xor_sync(both, am2, 1));
+    am2 = max2_nan(am2, am2 >> 16);
+    const uint8_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(bf16_lo(am2), 6.f * factor), __NV_SATFINITE, __NV_E4M3);
     const __half_raw hr = __nv_cvt_fp8_to_halfraw(sb, __NV_E4M3);
     const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
     uint32_t w = 0;
     if (s > 0.f) {  // false for 0 and NaN: zero codes
+        float x[8];
+        unpack8(v, x);
+        if (factor == 1.f) {
+            const float inv = __frcp_rn(s);
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float2 y = make_float2(__fdiv_rn(x[2 * e], s), __fdiv_rn(x[2 * e + 1], s));
-            w |= (uint32_t)__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest) << (8 * e);
+            for (int e = 0; e < 8; e++) x[e] = __uint_as_float((__float_as_uint(x[e] * inv) + 0x20u) & ~0x3fu);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) x[e] = __fdiv_rn(x[e], s);
         }
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e], x[2 * e + 1]), __NV_E2M1, cudaRoundNearest)
+                 << (8 * e);
     }
     *scale_byte = sb;
     return w;
@@ -81,15 +105,6 @@ __device__ __forceinline__ uint2 fp8_quantise8(const float* x, float scale) {
         packed[e >> 1] |= (b0 | (b1 << 8)) << (16 * (e & 1));
     }
     return make_uint2(packed[0], packed[1]);
-}
-
-__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        x[2 * e] = bf16_lo(ws[e]);
-        x[2 * e + 1] = bf16_hi(ws[e]);
-    }
 }
 
 __device__ __forceinline__ uint4 pack8(const float* x) {
@@ -114,10 +129,8 @@ __device__ __forceinline__ void store_gqa8(const AppendArgs& a, uint8_t* pool, i
             *reinterpret_cast<uint4*>(pool + ((((int64_t)pg * a.hkv + g) * P + off) * D + li * 8) * 2) = w;
         return;
     }
-    float x[8];
-    unpack8(w, x);
     uint8_t sb;
-    const uint32_t codes = fp4_quantise8(x, factor, both, &sb);
+    const uint32_t codes = fp4_quantise8(w, factor, both, &sb);
     if (!live) return;
     uint8_t* blk = pool + ((int64_t)pg * a.hkv + g) * fp4_block_bytes(P, D);
     *reinterpret_cast<uint32_t*>(blk + off * (D / 2) + li * 4) = codes;
