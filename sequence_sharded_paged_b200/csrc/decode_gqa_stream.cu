@@ -42,25 +42,28 @@
 // weights stay above fp16's smallest step.  With at most 8 query rows the two terms
 // share one instruction (rows 0..7 and 8..15 of the tile); with more they take two.
 #include <limits.h>
+#include <stdlib.h>
 
 #include "common.cuh"
 #include "finish.cuh"
 #include "kernels.h"
 #include "rows.cuh"
+#include "tma.h"
 
 namespace dcp {
 
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtasPerSm = 2;  // by registers and by the queues' sizes
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTok = 16;     // tokens per group
 constexpr int kDescs = 64;   // group descriptors per warp (two batches of 32)
 constexpr float kLazy = 8.f; // lazy rescale threshold (log2)
 
 // Launch constants of one cache type and head size.
-//   bf16: K 2 tiles x D/32 x 16 B, V 4 tokens x D/64 x 16 B a lane and group
-//   4-bit: K 2 tiles x D/8 B, V 4 tokens x D/16 B, scales (D/64 + 1) words
+//   bf16: K and V of 16 tokens, each [D/64 halves][16 tokens][128 B] with 128-byte swizzle
+//   4-bit, a lane and group: K 2 tiles x D/8 B, V 4 tokens x D/16 B, scales (D/64 + 1) words
 template <bool FP4, int D>
 struct Lane {
     static constexpr int kK = FP4 ? 2 * D / 8 : 2 * (D / 32) * 16;  // bytes of K
@@ -71,11 +74,12 @@ struct Lane {
     // what bounds it and two groups share the step's votes and hide each other's
     // latencies; bf16: one, since the bytes in flight are what counts.
     static constexpr int kStep = FP4 ? 2 : 1;
-    static constexpr int kSteps = FP4 ? (D == 128 ? 3 : 5) : (D == 128 ? 2 : 4);  // steps in the queue
+    static constexpr int kSteps = FP4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // steps in the queue
     static constexpr int kStages = kStep * kSteps;
 };
 
 struct StreamArgs {
+    alignas(64) CUtensorMap map_k, map_v;  // bf16: 4-D maps of the pools, boxes of one group
     const uint8_t* k_pages;
     const uint8_t* v_pages;
     const float* factors;  // 4-bit: {K, V} factors, or null
@@ -134,19 +138,28 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// orders this thread's writes to shared memory before later copies by the copy engine
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// d = a b + c
+template <bool FP4>
+__device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1, const float* c) {
+    if (FP4)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%10, %11, %12, %13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
 template <bool FP4>
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    if (FP4)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-            "{%0, %1, %2, %3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    mma<FP4>(d, a0, a1, a2, a3, b0, b1, d);
 }
 
 // the four bytes of w, two e2m1 values each, as four f16x2
@@ -255,14 +268,12 @@ __device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
     return max(v.count(lo, hi, a), 1);
 }
 
-// A group: byte offset of its first row in the pools (bf16) or of its block (4-bit),
-// -1: no page; first local token; shard; whether every row sees all of it.
+// A group: byte offset of its first row's codes in the pools (4-bit) or its index
+// page * hkv + head (bf16), -1: no page; first local token; shard.
 struct __align__(16) Desc {
     int64_t off;
     int t0;
-    int shard_full;
-    __device__ __forceinline__ int shard() const { return shard_full & 0x7fffffff; }
-    __device__ __forceinline__ bool full() const { return shard_full < 0; }
+    int shard;
 };
 
 __device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
@@ -298,8 +309,13 @@ struct Warp {
         l[0] = l[1] = 0.f;
     }
 
+    // bf16: which 16-byte chunk of a 128-byte half row thread column n holds; with the
+    // swizzle, the eight lanes of a shared-memory phase then hit eight different chunks
+    __device__ __forceinline__ static int chunk_of(int n) { return (n >> 1) | ((n & 1) << 2); }
     // first of the 8 dimensions that thread column n holds in n-tiles 8 w .. 8 w + 7
-    __device__ __forceinline__ static int dim_of(int n, int w) { return FP4 ? n * NT + 8 * w : (n + 8 * w) * 8; }
+    __device__ __forceinline__ static int dim_of(int n, int w) { return FP4 ? n * NT + 8 * w : (chunk_of(n) + 8 * w) * 8; }
+    // the four tokens that thread column c holds of P and V: x[t][e] is token_of(c, 2 t + e)
+    __device__ __forceinline__ static int token_of(int c, int i) { return FP4 ? 4 * c + i : c + 4 * i; }
 
     // Q fragments of rows qr (and qr + 8) of tile `tile` of KV head g
     __device__ __forceinline__ void load_q(const StreamArgs& a, int b, int g, int tile, int L, float kf) {
@@ -358,83 +374,89 @@ struct Warp {
         }
     }
 
-    // Start the copies of group d into queue slot `slot`.
-    __device__ __forceinline__ static void issue(const StreamArgs& a, const Desc& d, int L, uint32_t slot) {
-        if (d.off < 0) return;
-        bool live[6] = {true, true, true, true, true, true};  // K tiles' tokens, V's four tokens
-        if (d.full()) {
-            copy<false>(a, d, live, slot);
-            return;
+    // This thread's places in the pools (4-bit).
+    struct Places {
+        const uint8_t *k, *v, *ks, *vs;
+        int page;  // offset of the scales in a block, in rows of codes minus one
+        __device__ __forceinline__ explicit Places(const StreamArgs& a) {
+            const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+            const int P = a.page_size;
+            k = a.k_pages + (4 * (n >> 1) + (n & 1)) * (D / 2) + c * (D / 8);
+            v = a.v_pages + 4 * c * (D / 2) + n * (D / 16);
+            ks = a.k_pages + P * (D / 2) + (c * (D / 64)) * P + 4 * (n >> 1);
+            vs = a.v_pages + P * (D / 2) + (n * D / 128) * P + 4 * c;
+            page = P;
         }
+    };
+
+    // 4-bit: start the copies of group d, which not every row sees all of: a token is
+    // copied if any query token sees it, and is zeros otherwise.  Its scales come in
+    // words of four tokens; those of tokens that are not copied are cleared by the
+    // reader (`keep`).
+    __device__ __forceinline__ static void copy_masked(const StreamArgs& a, const Places& from, const Desc& d, int L,
+                                                       uint32_t slot) {
+        bool live[6];  // K tiles' tokens, V's four tokens
         const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
         const int first = L - a.q_len;
 #pragma unroll
-        for (int e = 0; e < 6; e++) {  // a token is copied if any query token sees it
+        for (int e = 0; e < 6; e++) {
             const int64_t p =
-                position_of(a, d.shard(), d.t0 + (e < 2 ? 4 * (n >> 1) + (n & 1) + 2 * e : 4 * c + e - 2));
-            live[e] = p < L && (p < a.sinks || first - p < a.window);
+                position_of(a, d.shard, d.t0 + (e < 2 ? 4 * (n >> 1) + (n & 1) + 2 * e : 4 * c + e - 2));
+            live[e] = d.off >= 0 && p < L && (p < a.sinks || first - p < a.window);
         }
-        copy<true>(a, d, live, slot);
+        Desc at = d;
+        if (d.off < 0) at.off = at.t0 = 0;  // no page: zeros, and block 0's scales (not used)
+        copy<true>(from, at, live, slot);
     }
 
     template <bool MASK>
-    __device__ __forceinline__ static void copy(const StreamArgs& a, const Desc& d, const bool* live, uint32_t slot) {
-        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        const int P = a.page_size;
-        const int kt = 4 * (n >> 1) + (n & 1);  // K: token of tile 0 (tile 1: + 2)
-        if (!FP4) {
-            const uint8_t* kb = a.k_pages + d.off + (kt * (D * 2) + c * 16);
-            const uint8_t* vb = a.v_pages + d.off + (4 * c * (D * 2) + n * 16);
-            const uint32_t dst = slot + lane * 16;
-#pragma unroll
-            for (int t = 0; t < 2; t++)
-#pragma unroll
-                for (int i = 0; i < D / 32; i++)
-                    cp16<MASK>(dst + (t * (D / 32) + i) * 512, kb + t * 2 * (D * 2) + i * 64, live[t]);
+    __device__ __forceinline__ static void copy(const Places& from, const Desc& d, const bool* live, uint32_t slot) {
+        const int lane = threadIdx.x & 31;
+        const int P = from.page;
+        // d.off is the group's first row of codes; its scales lie this much less than a row a token further
+        const int64_t so = d.off - (d.t0 & (P - 1)) * (D / 2 - 1);
+        const uint8_t *k = from.k + d.off, *v = from.v + d.off, *ks = from.ks + so, *vs = from.vs + so;
+        const uint32_t ds = slot + (C::kK + C::kV) * 32 + lane * 4;
+        if (D == 128) {
+            cp16<MASK>(slot + lane * 16, k, live[0]);
+            cp16<MASK>(slot + 512 + lane * 16, k + 2 * (D / 2), live[1]);
 #pragma unroll
             for (int e = 0; e < 4; e++)
-#pragma unroll
-                for (int i = 0; i < D / 64; i++)
-                    cp16<MASK>(dst + C::kK * 32 + (e * (D / 64) + i) * 512, vb + e * (D * 2) + i * 128, live[2 + e]);
+                cp8<MASK>(slot + 1024 + (e >> 1) * 512 + lane * 16 + (e & 1) * 8, v + e * (D / 2), live[2 + e]);
+            cp4<false>(ds, ks, true);
+            cp4<false>(ds + 128, ks + P, true);
+            cp4<false>(ds + 256, vs, true);
         } else {
-            const int sub = d.t0 & (P - 1);
-            const uint8_t* kb = a.k_pages + d.off;
-            const uint8_t* vb = a.v_pages + d.off;
-            const int kc = (sub + kt) * (D / 2) + c * (D / 8), vc = (sub + 4 * c) * (D / 2) + n * (D / 16);
-            // scale words hold four tokens; a token that is not copied has zero codes
-            const int ks = P * (D / 2) + (c * (D / 64)) * P + sub + 4 * (n >> 1);
-            const int vs = P * (D / 2) + (n * D / 128) * P + sub + 4 * c;
-            const uint32_t ds = slot + (C::kK + C::kV) * 32 + lane * 4;
-            if (D == 128) {
-                cp16<MASK>(slot + lane * 16, kb + kc, live[0]);
-                cp16<MASK>(slot + 512 + lane * 16, kb + kc + 2 * (D / 2), live[1]);
+            cp8<MASK>(slot + lane * 16, k, live[0]);
+            cp8<MASK>(slot + lane * 16 + 8, k + 2 * (D / 2), live[1]);
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    cp8<MASK>(slot + 1024 + (e >> 1) * 512 + lane * 16 + (e & 1) * 8, vb + vc + e * (D / 2),
-                              live[2 + e]);
-                cp4<false>(ds, kb + ks, true);
-                cp4<false>(ds + 128, kb + ks + P, true);
-                cp4<false>(ds + 256, vb + vs, true);
-            } else {
-                cp8<MASK>(slot + lane * 16, kb + kc, live[0]);
-                cp8<MASK>(slot + lane * 16 + 8, kb + kc + 2 * (D / 2), live[1]);
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    cp4<MASK>(slot + 512 + lane * 16 + e * 4, vb + vc + e * (D / 2), live[2 + e]);
-                cp4<false>(ds, kb + ks, true);
-                cp4<false>(ds + 128, vb + vs, true);
-            }
+            for (int e = 0; e < 4; e++) cp4<MASK>(slot + 512 + lane * 16 + e * 4, v + e * (D / 2), live[2 + e]);
+            cp4<false>(ds, ks, true);
+            cp4<false>(ds + 128, vs, true);
         }
     }
 
-    // V operands of n-tiles 8 w .. 8 w + 7: b[j][0] tokens 4c, 4c+1; b[j][1] tokens 4c+2, 4c+3
-    __device__ __forceinline__ static void load_v(const uint8_t* slot, int w, uint32_t (*b)[2]) {
+    // bf16: this thread's byte offsets in a stage: K, token (n >> 1) + 4 (n & 1) (+ 8 for
+    // tile 1), chunk 4 (i & 1) + c of half i / 2; V, token c + 4 e, chunk_of(n) of half w
+    __device__ __forceinline__ static int k_place(int t, int i) {
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        const int row = (n >> 1) + 4 * (n & 1);
+        return (i >> 1) * 2048 + (row + 8 * t) * 128 + (((c ^ row) << 4) ^ ((i & 1) << 6));
+    }
+    __device__ __forceinline__ static int v_place(int e, int w) {
+        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
+        return C::kK * 32 + w * 2048 + (c + 4 * e) * 128 + (((chunk_of(n) ^ c) << 4) ^ ((e & 1) << 6));
+    }
+
+    // V operands of n-tiles 8 w .. 8 w + 7: b[j][h] tokens token_of(c, 2h), token_of(c, 2h + 1).
+    // keep: bytes of the four tokens' scales that count
+    __device__ __forceinline__ static void load_v(const uint8_t* slot, int w, uint32_t keep, uint32_t (*b)[2]) {
         const int lane = threadIdx.x & 31;
         if (!FP4) {
             uint4 v[4];
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                v[e] = *reinterpret_cast<const uint4*>(slot + C::kK * 32 + (e * (D / 64) + w) * 512 + lane * 16);
+                v[e] = *reinterpret_cast<const uint4*>(slot + v_place(e, w));
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 const uint32_t x[4] = {v[2 * h].x, v[2 * h].y, v[2 * h].z, v[2 * h].w};
@@ -453,7 +475,7 @@ struct Warp {
                                                                      (e & 1) * 8 + w * 4)
                                 : *reinterpret_cast<const uint32_t*>(slot + 512 + lane * 16 + e * 4);
             const uint32_t sw =
-                *reinterpret_cast<const uint32_t*>(slot + (C::kK + C::kV) * 32 + (D / 64) * 128 + lane * 4);
+                keep & *reinterpret_cast<const uint32_t*>(slot + (C::kK + C::kV) * 32 + (D / 64) * 128 + lane * 4);
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 // low half of a byte: token 4c + 2h, high half: the next token, same dimension
@@ -471,17 +493,15 @@ struct Warp {
         }
     }
 
-    // Scores of one group: x[t][e], e = 0, 1: row qr, token 4c + 2t + e; e = 2, 3: row qr + 8
+    // Scores of one group: x[t][e], e = 0, 1: row qr, token_of(c, 2t + e); e = 2, 3: row qr + 8
     __device__ __forceinline__ void scores(const uint8_t* slot, float (*x)[4]) {
         const int lane = threadIdx.x & 31, n = lane >> 2;
-#pragma unroll
-        for (int t = 0; t < 2; t++) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
         if (!FP4) {
 #pragma unroll
             for (int i = 0; i < D / 32; i++)
 #pragma unroll
                 for (int t = 0; t < 2; t++) {
-                    const uint4 k = *reinterpret_cast<const uint4*>(slot + (t * (D / 32) + i) * 512 + lane * 16);
+                    const uint4 k = *reinterpret_cast<const uint4*>(slot + k_place(t, i));
                     qk(x[t], 2 * i, k.x, k.y);
                     qk(x[t], 2 * i + 1, k.z, k.w);
                 }
@@ -512,23 +532,44 @@ struct Warp {
         }
     }
 
-    // G groups (slots slot[0 .. G-1]): scores, one softmax step, O += P V.  MASK: one
-    // group that not every row sees all of.
-    template <int G, bool MASK>
-    __device__ __forceinline__ void consume(const StreamArgs& a, const Desc& d, const uint8_t* const* slot) {
-        const int c = threadIdx.x & 3;
-        float x[2 * G][4];
+    static constexpr int G = C::kStep;
+
+    // Scores of a step whose groups lie in consecutive slots.
+    __device__ __forceinline__ void step_scores(const uint8_t* at, float (*x)[4]) {
 #pragma unroll
-        for (int g = 0; g < G; g++) scores(slot[g], x + 2 * g);
-        if (MASK) {
+        for (int g = 0; g < G; g++) scores(at + g * C::kStage, x + 2 * g);
+    }
+
+    // Masks of a step that not every row sees all of: scores of what a row does not
+    // see become -inf; of tokens that no row sees, keep[g] clears the scales (4-bit) and
+    // the values are set to zero in the stage (bf16: each thread's own chunks).
+    __device__ __forceinline__ void mask(const StreamArgs& a, const Desc* d, int L, uint8_t* stage, float (*x)[4],
+                                         uint32_t* keep) {
+        const int c = threadIdx.x & 3, first = L - a.q_len;
 #pragma unroll
-            for (int e = 0; e < 4; e++) {  // token 4c + e
-                const int64_t p = position_of(a, d.shard(), d.t0 + 4 * c + e);
+        for (int g = 0; g < G; g++) {
+            keep[g] = 0;
+            const bool page = d[g].off >= 0;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const int64_t p = position_of(a, d[g].shard, d[g].t0 + token_of(c, e));
+                if (page && p < L && (p < a.sinks || first - p < a.window)) {
+                    keep[g] |= 0xffu << (8 * e);
+                } else if (!FP4) {
+#pragma unroll
+                    for (int w = 0; w < NT / 8; w++)
+                        *reinterpret_cast<uint4*>(stage + v_place(e, w)) = make_uint4(0u, 0u, 0u, 0u);
+                }
 #pragma unroll
                 for (int h = 0; h < H; h++)
-                    if (!sees(a, p, at[h])) x[e >> 1][2 * h + (e & 1)] = -INFINITY;
+                    if (!page || !sees(a, p, at[h])) x[2 * g + (e >> 1)][2 * h + (e & 1)] = -INFINITY;
             }
         }
+        if (!FP4) fence_async();  // before the stage's next copy
+    }
+
+    // One softmax step: x becomes the A operands of P V (hi + lo terms), [row half + 2 * tile].
+    __device__ __forceinline__ void softmax(const float (*x)[4], uint32_t (*hi)[4], uint32_t (*lo)[4]) {
         float mx[H];
         bool grow = false;
 #pragma unroll
@@ -536,8 +577,7 @@ struct Warp {
             mx[h] = -INFINITY;
 #pragma unroll
             for (int t = 0; t < 2 * G; t++) mx[h] = fmaxf(mx[h], fmaxf(x[t][2 * h], x[t][2 * h + 1]));
-            // scale = 0 (a query of zeros has scale > 0; the caller's scale may be 0): 0 * -inf stays masked
-            mx[h] = mx[h] == -INFINITY ? -INFINITY : mx[h] * scale[h];
+            mx[h] *= scale[h];
             grow |= mx[h] > m[h] + (kLazy + kBias);
         }
         if (__any_sync(0xffffffffu, grow)) {
@@ -555,21 +595,16 @@ struct Warp {
                 }
             }
         }
-        uint32_t hi[G][4], lo[G][4];  // A operands: [row half + 2 * tile]
 #pragma unroll
         for (int h = 0; h < H; h++) {
             const float ref = m[h] == -INFINITY ? 0.f : m[h];
             float sum = 0.f;
 #pragma unroll
             for (int t = 0; t < 2 * G; t++) {
-                float p[2];
-#pragma unroll
-                for (int e = 0; e < 2; e++) {
-                    p[e] = fast_exp2(fmaf(x[t][2 * h + e], scale[h], -ref));
-                    if (MASK && x[t][2 * h + e] == -INFINITY) p[e] = 0.f;  // also where the scale is 0
-                }
-                sum += p[0] + p[1];
-                split2<FP4>(p[0], p[1], hi[t >> 1][h + 2 * (t & 1)], lo[t >> 1][h + 2 * (t & 1)]);
+                const float p0 = fast_exp2(fmaf(x[t][2 * h], scale[h], -ref));
+                const float p1 = fast_exp2(fmaf(x[t][2 * h + 1], scale[h], -ref));
+                sum += p0 + p1;
+                split2<FP4>(p0, p1, hi[t >> 1][h + 2 * (t & 1)], lo[t >> 1][h + 2 * (t & 1)]);
             }
             l[h] += sum;
         }
@@ -580,16 +615,17 @@ struct Warp {
                 hi[g][3] = lo[g][2];
             }
         }
-        if (MASK && a.q_len > 1 && poisoned(slot[0])) {
-            careful(a, d, slot[0], hi[0], lo[0]);
-            return;
-        }
+    }
+
+    // O += P V
+    __device__ __forceinline__ void values(const uint8_t* at, const uint32_t* keep, const uint32_t (*hi)[4],
+                                           const uint32_t (*lo)[4]) {
 #pragma unroll
         for (int g = 0; g < G; g++) {
 #pragma unroll
             for (int w = 0; w < NT / 8; w++) {
                 uint32_t b[8][2];
-                load_v(slot[g], w, b);
+                load_v(at + g * C::kStage, w, keep[g], b);
 #pragma unroll
                 for (int j = 0; j < 8; j++)
                     mma<FP4>(o[8 * w + j], hi[g][0], hi[g][1], hi[g][2], hi[g][3], b[j][0], b[j][1]);
@@ -623,19 +659,21 @@ struct Warp {
     }
 
     __device__ __forceinline__ void qk(float* d, int s, uint32_t b0, uint32_t b1) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        const float* c = s == 0 ? zero : d;
         if (HALF)
-            mma<FP4>(d, q[s][0], 0u, q[s][1], 0u, b0, b1);
+            mma<FP4>(d, q[s][0], 0u, q[s][1], 0u, b0, b1, c);
         else
-            mma<FP4>(d, q[s][0], q[s][1], q[s][HALF ? 0 : 2], q[s][HALF ? 0 : 3], b0, b1);
+            mma<FP4>(d, q[s][0], q[s][1], q[s][HALF ? 0 : 2], q[s][HALF ? 0 : 3], b0, b1, c);
     }
 
     // Does the group hold an infinity or NaN among its values?
-    __device__ __forceinline__ static bool poisoned(const uint8_t* slot) {
+    __device__ __forceinline__ static bool poisoned(const uint8_t* slot, uint32_t keep) {
         bool bad = false;
 #pragma unroll 1
         for (int w = 0; w < NT / 8; w++) {
             uint32_t b[8][2];
-            load_v(slot, w, b);
+            load_v(slot, w, keep, b);
             constexpr uint32_t e = FP4 ? 0x7c00u : 0x7f80u;
 #pragma unroll
             for (int j = 0; j < 8; j++)
@@ -646,34 +684,35 @@ struct Warp {
         return __any_sync(0xffffffffu, bad);
     }
 
-    // P V where some rows must not see a non-finite value that others see: row by
-    // row, with the values that the row does not see set to zero.
-    __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot,
+    // O += P V of one group where some rows must not see a non-finite value that
+    // others see: row by row, with the values that the row does not see set to zero.
+    __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot, uint32_t keep,
                                             const uint32_t* hi, const uint32_t* lo) {
         const int lane = threadIdx.x & 31, qr = lane >> 2;
 #pragma unroll 1
         for (int r = 0; r < (HALF ? 8 : 16); r++) {
             // the position of row r, from a lane that holds it
             const int at_r = __shfl_sync(0xffffffffu, r < 8 ? at[0] : at[1], (r & 7) * 4);
-            uint32_t keep[2];
+            uint32_t sees_v[2];
 #pragma unroll
             for (int h = 0; h < 2; h++) {
-                keep[h] = 0;
+                sees_v[h] = 0;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int64_t p = position_of(a, d.shard(), d.t0 + 4 * (lane & 3) + 2 * h + e);
-                    if (sees(a, p, at_r)) keep[h] |= 0xffffu << (16 * e);
+                    const int64_t p = position_of(a, d.shard, d.t0 + token_of(lane & 3, 2 * h + e));
+                    if (d.off >= 0 && sees(a, p, at_r)) sees_v[h] |= 0xffffu << (16 * e);
                 }
             }
 #pragma unroll
             for (int w = 0; w < NT / 8; w++) {
                 uint32_t b[8][2];
-                load_v(slot, w, b);
+                load_v(slot, w, keep, b);
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    float t[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma<FP4>(t, hi[0], hi[1], hi[2], hi[3], b[j][0] & keep[0], b[j][1] & keep[1]);
-                    if (!HALF) mma<FP4>(t, lo[0], lo[1], lo[2], lo[3], b[j][0] & keep[0], b[j][1] & keep[1]);
+                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                    float t[4];
+                    mma<FP4>(t, hi[0], hi[1], hi[2], hi[3], b[j][0] & sees_v[0], b[j][1] & sees_v[1], zero);
+                    if (!HALF) mma<FP4>(t, lo[0], lo[1], lo[2], lo[3], b[j][0] & sees_v[0], b[j][1] & sees_v[1]);
                     if (qr == (r & 7)) {
 #pragma unroll
                         for (int e = 0; e < 4; e++)
@@ -718,9 +757,10 @@ __device__ __forceinline__ Row out_row(const StreamArgs& a, int base, int g, int
     return Row{a.out + at * D, a.lse + at};
 }
 
-// min blocks per SM: three CTAs of four warps at 168 registers
+// Two CTAs of four warps for each SM: what hides latency here is independent work
+// within a warp, which takes registers, more than a third CTA would.
 template <bool FP4, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
     using W = Warp<FP4, D, HALF>;
     using C = Lane<FP4, D>;
     constexpr int S = C::kStages;
@@ -728,7 +768,12 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
     constexpr int kRows = HALF ? 8 : 16;
     constexpr int kPitch = D + 4;  // floats a row of O in the team merge
     static_assert(kRing >= kRows * kPitch * 4, "a warp's queue holds its O");
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    // the swizzle of the bf16 stages goes by the address: 1024-byte alignment
+    uint8_t* smem = FP4 ? smem_raw
+                        : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t s_full[kWarps][C::kSteps];  // bf16: a stage's copies have landed
+    __shared__ volatile int s_abort;
     __shared__ Desc s_desc[kWarps][kDescs];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_ol[kWarps][16];
     __shared__ long long s_scan[kWarps];
@@ -746,6 +791,18 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
     const int per_base = a.hkv * a.tiles;
     const float kf = FP4 && a.factors ? __ldg(a.factors) : 1.f, vf = FP4 && a.factors ? __ldg(a.factors + 1) : 1.f;
 
+    if (!FP4) {
+        if (lane == 0) {
+            for (int k = 0; k < C::kSteps; k++) mbar_init(&s_full[warp][k], 1);
+            fence_barrier_init();
+        }
+        if (threadIdx.x == 0) {
+            s_abort = 0;
+            tma_prefetch_desc(&a.map_k);
+            tma_prefetch_desc(&a.map_v);
+        }
+        __syncthreads();
+    }
     if (blockIdx.x == 0)
         for (int b = threadIdx.x; b < a.batch; b += kThreads) {
             const int L = __ldg(a.seq_lens + b);
@@ -808,6 +865,9 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
             x0 = s_off[team];
         }
     }
+    const typename W::Places places(a);
+    uint32_t issued = 0, landed = 0;  // bf16: steps issued, and waited for
+    uint32_t started = 0;             // lane 0: issued steps whose copies were started (all, but after a timeout)
     int4 tail = make_int4(-1, 0, 0, 0);
     long long pos = r0;
     long long seg = worker;
@@ -839,10 +899,13 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
         if (take > 0) {
         const int nk = wt < take ? (take - wt + a.team - 1) / a.team : 0;  // this warp's groups
 
+        // bit k % 32: every row sees all of group k (of the even and the odd batches); clear past the last group
+        uint32_t full0 = 0, full1 = 0;
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
             const int k = 32 * kb + lane;
             Desc d{-1, 0, 0};
+            bool whole_group = false;
             int i = i0 + wt + a.team * k;
             if (k < nk && i < real) {
                 int n = lo;
@@ -862,57 +925,120 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
                 if (pg < 0 || pg >= a.num_pages)
                     record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
                 else
-                    d.off = ((int64_t)pg * a.hkv + g) * (FP4 ? fp4_block_bytes(P, D) : P * D * 2) +
-                            (FP4 ? 0 : (d.t0 & (P - 1)) * D * 2);
+                    d.off = ((int64_t)pg * a.hkv + g) * (FP4 ? fp4_block_bytes(P, D) : 1) +
+                            (FP4 ? (d.t0 & (P - 1)) * (D / 2) : 0);
                 const int64_t p0 = position_of(a, n, d.t0), p1 = position_of(a, n, d.t0 + kTok - 1);
                 const bool full = pg >= 0 && p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p0 < a.window);
-                d.shard_full = n | (full && d.off >= 0 ? 0x80000000 : 0);
+                d.shard = n;
+                whole_group = full;
             }
-            __syncwarp();
+            const uint32_t mask = __ballot_sync(0xffffffffu, whole_group);
+            if (kb & 1)
+                full1 = mask;
+            else
+                full0 = mask;
             descs[(kb & 1) * 32 + lane] = d;
             __syncwarp();
         };
+        // are the groups of the step at k all seen whole by every row?
+        auto step_full = [&](int k) {
+            constexpr uint32_t m = (1u << C::kStep) - 1u;
+            return (((k & 32 ? full1 : full0) >> (k & 31)) & m) == m;
+        };
 
-        if (nk > 0) batch(0);
-        auto start = [&](int k, int slot) {  // copies of one step, as one commit group
-#pragma unroll
-            for (int e = 0; e < C::kStep; e++)
-                if (k + e < nk) {
-                    if (k + e > 0 && ((k + e) & 31) == 0) batch((k + e) >> 5);
-                    W::issue(a, descs[(k + e) & (kDescs - 1)], L, ring_u32 + (slot + e) * C::kStage);
+        auto start = [&](int k, int slot) {  // copies of one step
+            if ((k & 31) == 0) batch(k >> 5);
+            const Desc* d = descs + (k & (kDescs - 1));
+            if (!FP4) {  // slots and phases run on from segment to segment
+                if (k >= nk) return;
+                __syncwarp();  // every lane is done with the stage
+                if (lane == 0 && !s_abort) {
+                    const uint32_t at = issued % C::kSteps;
+                    uint8_t* stage = ring + at * C::kStage;
+                    uint64_t* bar = &s_full[warp][at];
+                    if (d->off >= 0) {
+                        const int row = (int)d->off, y = d->t0 & (a.page_size - 1);
+                        mbar_arrive_expect_tx(bar, C::kStage);
+                        tma_load_4d(stage, &a.map_k, 0, y, 0, row, bar);
+                        tma_load_4d(stage + C::kK * 32, &a.map_v, 0, y, 0, row, bar);
+                    } else {
+                        mbar_arrive(bar);
+                    }
+                    started = issued + 1;
                 }
+                issued++;
+                return;
+            }
+            if (step_full(k)) {
+                const bool live[6] = {true, true, true, true, true, true};
+#pragma unroll
+                for (int e = 0; e < C::kStep; e++)
+                    W::template copy<false>(places, d[e], live, ring_u32 + (slot + e) * C::kStage);
+            } else {
+#pragma unroll 1
+                for (int e = 0; e < C::kStep; e++)
+                    W::copy_masked(a, places, d[e], L, ring_u32 + (slot + e) * C::kStage);
+            }
             cp_commit();
         };
-#pragma unroll
+        // wait for step k and return its stage
+        auto arrived = [&](int k, int slot) -> uint8_t* {
+            if (FP4) {
+                cp_wait<C::kSteps - 2>();
+                return ring + slot * C::kStage;
+            }
+            const uint32_t at = landed % C::kSteps;
+            if (k < nk) {  // on a timeout the copies' bytes are used as they are: the call's outputs are unspecified
+                mbar_wait(&s_full[warp][at], (landed / C::kSteps) & 1, &s_abort, a.status);
+                landed++;
+            }
+            return ring + at * C::kStage;
+        };
+#pragma unroll 1
         for (int k = 0; k < C::kSteps - 1; k++) start(k * C::kStep, k * C::kStep);
         st.reset();
         st.load_q(a, b, g, tile, L, kf);
+        // Software pipeline: the scores of step k + 1 are computed beside P V of step k,
+        // two independent streams of matrix instructions.  (Past the last step the
+        // scores are of leftover bytes and nobody reads them.)
         int slot_in = (C::kSteps - 1) * C::kStep, slot_out = 0;
+        float x[2 * C::kStep][4];
+        uint8_t* here = arrived(0, 0);
+        st.step_scores(here, x);
+#pragma unroll 1
         for (int k = 0; k < nk; k += C::kStep) {
             start(k + (C::kSteps - 1) * C::kStep, slot_in);
             if ((slot_in += C::kStep) == S) slot_in = 0;
-            cp_wait<C::kSteps - 1>();
-            const uint8_t* at = ring + slot_out * C::kStage;
+            uint8_t* at = here;
             if ((slot_out += C::kStep) == S) slot_out = 0;
-            const Desc d0 = descs[k & (kDescs - 1)];
-            if (C::kStep == 1) {
-                if (d0.full())
-                    st.template consume<1, false>(a, d0, &at);
-                else if (d0.off >= 0)
-                    st.template consume<1, true>(a, d0, &at);
+            here = arrived(k + C::kStep, slot_out);
+            const Desc* d = descs + (k & (kDescs - 1));
+            uint32_t keep[C::kStep], hi[C::kStep][4], lo[C::kStep][4];
+#pragma unroll
+            for (int e = 0; e < C::kStep; e++) keep[e] = 0xffffffffu;
+            const bool full = step_full(k);
+            if (!full) st.mask(a, d, L, at, x, keep);
+            st.softmax(x, hi, lo);
+            bool safe = true;
+            if (!full && a.q_len > 1) {
+#pragma unroll
+                for (int e = 0; e < C::kStep; e++) safe &= !W::poisoned(at + e * C::kStage, keep[e]);
+            }
+            if (safe) {
+                st.step_scores(here, x);
+                st.values(at, keep, hi, lo);
             } else {
-                const uint8_t* two[2] = {at, at + C::kStage};
-                const Desc d1 = descs[(k + 1) & (kDescs - 1)];
-                if (k + 1 < nk && d0.full() && d1.full()) {
-                    st.template consume<2, false>(a, d0, two);
-                } else {
 #pragma unroll 1
-                    for (int e = 0; e < 2 && k + e < nk; e++) {
-                        const Desc d = descs[(k + e) & (kDescs - 1)];
-                        const uint8_t* one = at + e * C::kStage;
-                        if (d.off >= 0) st.template consume<1, true>(a, d, &one);
+                for (int e = 0; e < C::kStep; e++) {
+                    uint32_t h[4], w[4];  // chosen without an index, so that hi and lo stay in registers
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        h[i] = e ? hi[C::kStep - 1][i] : hi[0][i];
+                        w[i] = e ? lo[C::kStep - 1][i] : lo[0][i];
                     }
+                    st.careful(a, d[e], at + e * C::kStage, e ? keep[C::kStep - 1] : keep[0], h, w);
                 }
+                st.step_scores(here, x);
             }
         }
         cp_wait<0>();
@@ -965,6 +1091,7 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
                         *reinterpret_cast<float4*>(so + r * kPitch + W::dim_of(2 * c + e, j / 8) + (j & 7)) =
                             make_float4(st.o[j][2 * h + e], st.o[j + 1][2 * h + e], st.o[j + 2][2 * h + e],
                                         st.o[j + 3][2 * h + e]);
+                if (!FP4) fence_async();
                 if (c == 0) {
                     s_m[warp][r] = st.m[h];
                     s_l[warp][r] = st.l[h];
@@ -1023,6 +1150,10 @@ __global__ void __launch_bounds__(kThreads, 3) gqa_stream_kernel(const __grid_co
         }
     }
     if (!a.whole && wt == 0 && lane == 0) a.tail[worker] = tail;
+    // after a timeout copies may still be in flight: wait for them, bounded, before the block's memory is given up
+    if (!FP4 && lane == 0 && s_abort)
+        for (uint32_t k = started < C::kSteps ? 0 : started - C::kSteps; k < started; k++)
+            mbar_wait(&s_full[warp][k % C::kSteps], (k / C::kSteps) & 1, nullptr, a.status);
 }
 
 // Sum of a segment's parts: worker w's tail and the heads of the workers after it up
@@ -1087,15 +1218,13 @@ __global__ void finish_init_kernel(int64_t* finish_ns, int64_t* t_start, int B) 
 
 template <bool FP4, int D, bool HALF>
 cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
-    constexpr int smem = kWarps * Lane<FP4, D>::kStages * Lane<FP4, D>::kStage;
+    constexpr int smem = kWarps * Lane<FP4, D>::kStages * Lane<FP4, D>::kStage + (FP4 ? 0 : 1024);
     // once per process and device would do; the call is cheap and keeps no state
     cudaError_t e = cudaFuncSetAttribute(gqa_stream_kernel<FP4, D, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     gqa_stream_kernel<FP4, D, HALF><<<ctas, kThreads, smem, s>>>(a);
     return cudaGetLastError();
 }
-
-constexpr int kCtasPerSm = 3;  // of the launch bounds and the queues' sizes
 
 }  // namespace
 
@@ -1135,6 +1264,8 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
     p.lead = p.team == 1 ? 2 : 8;
+    if (getenv("ST_TEAM") && !p.whole) p.team = atoi(getenv("ST_TEAM"));
+    if (getenv("ST_LEAD")) p.lead = atoi(getenv("ST_LEAD"));
     int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
     if (grid > ctas) grid = ctas;
     p.ctas = (int)grid;
@@ -1206,6 +1337,17 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     }
     const bool fp4 = c->dtype == DCP_FP4_E2M1, half = a.rows <= 8;
     cudaError_t e;
+    if (!fp4) {
+        // the pools as [page * hkv + head][64-column half][token][64 columns]; a box is 16 tokens of one head
+        const uint64_t dims[4] = {64, (uint64_t)c->page_size, (uint64_t)(c->dk / 64), (uint64_t)c->num_pages * c->hkv};
+        const uint64_t strides[3] = {(uint64_t)c->dk * 2, 128, (uint64_t)c->page_size * c->dk * 2};
+        const uint32_t box[4] = {64, (uint32_t)kTok, (uint32_t)(c->dk / 64), 1};
+        if (!make_tmap_4d(&a.map_k, c->k_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_tmap_4d(&a.map_v, c->v_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+            return cudaErrorInvalidValue;
+    }
     if (c->dk == 64) {
         if (fp4)
             e = half ? run<true, 64, true>(a, p.ctas, s) : run<true, 64, false>(a, p.ctas, s);
