@@ -147,90 +147,116 @@ __global__ void append_mla_fp8_kernel(AppendArgs a) {
     if (lane == 0) a.kv_scales[(int64_t)pg * a.page_size + off] = scale;
 }
 
-// GQA, 4-bit: D/8 lanes per token, 8 dimensions each; a lane pair shares the
-// scale of its 16 dimensions.  The token's page is looked up once for up to
-// kHeadsPerLane heads, whose K and V rows are all loaded before any is
-// quantised.  Bound by HBM: 4 D bytes in and 2 (D/2 + D/16) out for each head.
+// GQA, 4-bit: D/16 lanes per token, a run of 16 dimensions (one scale) each.  The
+// token's page is looked up once for up to kHeadsPerLane heads, whose K and V rows are
+// all loaded before any is quantised.  The floor is HBM's, 4 D bytes in and
+// 2 (D/2 + D/16) out for each head; what bounds it is the arithmetic of the codes.
 constexpr int kHeadsPerLane = 2;
 
-__global__ void __launch_bounds__(256, 6) append_gqa_fp4_kernel(AppendArgs a) {
-    const int lpr = a.dk / 8;
+struct RowLane {
+    int64_t i;  // token
+    int g0;     // first head
+    int li;     // run of dimensions
+    int pg, off;
+};
+
+__device__ __forceinline__ RowLane row_lane(const AppendArgs& a) {
+    const int lpr = a.dk / 16;
     const int hb = (a.hkv + kHeadsPerLane - 1) / kHeadsPerLane;
     const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
-    const int li = threadIdx.x % lpr;
-    const int64_t i = w / hb;
-    const int g0 = (int)(w - i * hb) * kHeadsPerLane;
-    int off = 0;
-    const int pg = i < a.n_tok ? append_target(a, i, &off) : -2;
-    if (pg == -1 && li == 0 && g0 == 0) record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
-    // the lanes of a pair always agree on pg; pairs drop out together
-    const uint32_t both = __ballot_sync(0xffffffffu, pg >= 0);
-    if (pg < 0) return;
-    const float fk = a.kv_scales ? __ldg(a.kv_scales) : 1.f, fv = a.kv_scales ? __ldg(a.kv_scales + 1) : 1.f;
-    uint4 k[kHeadsPerLane], v[kHeadsPerLane];
-#pragma unroll
-    for (int e = 0; e < kHeadsPerLane; e++) {
-        const int g = min(g0 + e, a.hkv - 1);
-        k[e] = __ldg(reinterpret_cast<const uint4*>(a.k_new + ((i * a.hkv + g) * a.dk + li * 8) * 2));
-        v[e] = __ldg(reinterpret_cast<const uint4*>(a.v_new + ((i * a.hkv + g) * a.dk + li * 8) * 2));
-    }
-#pragma unroll
-    for (int e = 0; e < kHeadsPerLane; e++) {
-        const bool live = g0 + e < a.hkv;
-        store_gqa8(a, a.k_pages, pg, g0 + e, off, li, k[e], fk, both, live);
-        store_gqa8(a, a.v_pages, pg, g0 + e, off, li, v[e], fv, both, live);
-    }
+    RowLane r{w / hb, 0, (int)(threadIdx.x % lpr), -2, 0};
+    r.g0 = (int)(w - r.i * hb) * kHeadsPerLane;
+    if (r.i < a.n_tok) r.pg = append_target(a, r.i, &r.off);
+    if (r.pg == -1 && r.li == 0 && r.g0 == 0) record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
+    return r;
 }
 
-// 8 values of a 4-bit row as bf16.
-__device__ __forceinline__ uint4 load_fp4x8(const uint8_t* blk, int P, int D, int off, int li, float factor) {
-    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(blk + off * (D / 2) + li * 4));
-    const __half_raw hr = __nv_cvt_fp8_to_halfraw(__ldg(blk + P * (D / 2) + (li >> 1) * P + off), __NV_E4M3);
-    const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const __half2_raw h2 = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(codes >> (8 * e)), __NV_E2M1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-        x[2 * e] = f.x * s;
-        x[2 * e + 1] = f.y * s;
-    }
-    return pack8(x);
+__device__ __forceinline__ void store_fp4x16(uint8_t* blk, int P, int D, int off, int li, const uint4* v,
+                                             float factor) {
+    float s;
+    const uint8_t sb = fp4_scale(max2_nan(fp4_abs_max(v[0]), fp4_abs_max(v[1])), factor, &s);
+    *reinterpret_cast<uint2*>(blk + off * (D / 2) + li * 8) =
+        make_uint2(fp4_codes8(v[0], s, factor), fp4_codes8(v[1], s, factor));
+    blk[P * (D / 2) + li * P + off] = sb;
 }
 
-// Read-back, GQA: the append's lanes in reverse (bf16 or 4-bit pools).
-__global__ void __launch_bounds__(256, 6) gather_gqa_kernel(AppendArgs a, uint8_t* k_out, uint8_t* v_out) {
-    const int lpr = a.dk / 8;
-    const int hb = (a.hkv + kHeadsPerLane - 1) / kHeadsPerLane;
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
-    const int li = threadIdx.x % lpr;
-    const int64_t i = w / hb;
-    const int g0 = (int)(w - i * hb) * kHeadsPerLane;
-    if (i >= a.n_tok) return;
-    int off = 0;
-    const int pg = append_target(a, i, &off);
-    if (pg == -1 && li == 0 && g0 == 0) record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
-    if (pg < 0) return;
+__global__ void __launch_bounds__(256, 4) append_gqa_fp4_kernel(AppendArgs a) {
+    const RowLane r = row_lane(a);
+    if (r.pg < 0) return;
     const int P = a.page_size, D = a.dk;
     const float fk = a.kv_scales ? __ldg(a.kv_scales) : 1.f, fv = a.kv_scales ? __ldg(a.kv_scales + 1) : 1.f;
-    uint4 k[kHeadsPerLane], v[kHeadsPerLane];
+    uint4 k[kHeadsPerLane][2], v[kHeadsPerLane][2];
 #pragma unroll
     for (int e = 0; e < kHeadsPerLane; e++) {
-        const int64_t row = (int64_t)pg * a.hkv + min(g0 + e, a.hkv - 1);
-        if (a.dtype == DCP_BF16) {
-            k[e] = __ldg(reinterpret_cast<const uint4*>(a.k_pages + ((row * P + off) * D + li * 8) * 2));
-            if (v_out) v[e] = __ldg(reinterpret_cast<const uint4*>(a.v_pages + ((row * P + off) * D + li * 8) * 2));
-        } else {
-            k[e] = load_fp4x8(a.k_pages + row * fp4_block_bytes(P, D), P, D, off, li, fk);
-            if (v_out) v[e] = load_fp4x8(a.v_pages + row * fp4_block_bytes(P, D), P, D, off, li, fv);
+        if (r.g0 + e >= a.hkv) break;
+        const int64_t at = ((r.i * a.hkv + r.g0 + e) * D + r.li * 16) * 2;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            k[e][h] = __ldg(reinterpret_cast<const uint4*>(a.k_new + at) + h);
+            v[e][h] = __ldg(reinterpret_cast<const uint4*>(a.v_new + at) + h);
         }
     }
 #pragma unroll
     for (int e = 0; e < kHeadsPerLane; e++) {
-        if (g0 + e >= a.hkv) break;
-        const int64_t at = ((i * a.hkv + g0 + e) * D + li * 8) * 2;
-        *reinterpret_cast<uint4*>(k_out + at) = k[e];
-        if (v_out) *reinterpret_cast<uint4*>(v_out + at) = v[e];
+        if (r.g0 + e >= a.hkv) break;
+        const int64_t blk = ((int64_t)r.pg * a.hkv + r.g0 + e) * fp4_block_bytes(P, D);
+        store_fp4x16(a.k_pages + blk, P, D, r.off, r.li, k[e], fk);
+        store_fp4x16(a.v_pages + blk, P, D, r.off, r.li, v[e], fv);
+    }
+}
+
+// 16 values of a 4-bit row as bf16.
+__device__ __forceinline__ void unpack_fp4x16(uint2 codes, uint8_t scale, float factor, uint4* out) {
+    const __half_raw hr = __nv_cvt_fp8_to_halfraw(scale, __NV_E4M3);
+    const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+        const uint32_t c = h ? codes.y : codes.x;
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const __half2_raw h2 = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(c >> (8 * e)), __NV_E2M1);
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+            x[2 * e] = f.x * s;
+            x[2 * e + 1] = f.y * s;
+        }
+        out[h] = pack8(x);
+    }
+}
+
+// Read-back, GQA: the append's lanes in reverse.
+template <bool FP4>
+__global__ void __launch_bounds__(256, FP4 ? 6 : 4) gather_gqa_kernel(AppendArgs a, uint8_t* k_out, uint8_t* v_out) {
+    const RowLane r = row_lane(a);
+    if (r.pg < 0) return;
+    const int P = a.page_size, D = a.dk;
+    const float fk = FP4 && a.kv_scales ? __ldg(a.kv_scales) : 1.f, fv = FP4 && a.kv_scales ? __ldg(a.kv_scales + 1) : 1.f;
+    const uint8_t* pools[2] = {a.k_pages, a.v_pages};
+    uint8_t* outs[2] = {k_out, v_out};
+    uint4 w[2 * kHeadsPerLane][2];  // bf16: the row's bytes; 4-bit: codes in x, y and the scale in z
+#pragma unroll
+    for (int e = 0; e < 2 * kHeadsPerLane; e++) {
+        const int g = r.g0 + (e >> 1);
+        if (g >= a.hkv || !outs[e & 1]) continue;
+        const int64_t row = (int64_t)r.pg * a.hkv + g;
+        if (FP4) {
+            const uint8_t* blk = pools[e & 1] + row * fp4_block_bytes(P, D);
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(blk + r.off * (D / 2) + r.li * 8));
+            w[e][0] = make_uint4(c.x, c.y, __ldg(blk + P * (D / 2) + r.li * P + r.off), 0);
+        } else {
+            const uint4* src = reinterpret_cast<const uint4*>(pools[e & 1] + ((row * P + r.off) * D + r.li * 16) * 2);
+            w[e][0] = __ldg(src);
+            w[e][1] = __ldg(src + 1);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2 * kHeadsPerLane; e++) {
+        const int g = r.g0 + (e >> 1);
+        if (g >= a.hkv || !outs[e & 1]) continue;
+        if (FP4) unpack_fp4x16(make_uint2(w[e][0].x, w[e][0].y), (uint8_t)w[e][0].z, e & 1 ? fv : fk, w[e]);
+        uint4* dst = reinterpret_cast<uint4*>(outs[e & 1] + ((r.i * a.hkv + g) * D + r.li * 16) * 2);
+        dst[0] = w[e][0];
+        dst[1] = w[e][1];
     }
 }
 
@@ -291,7 +317,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     if (a.n_tok == 0) return cudaSuccess;
     if (a.dtype == DCP_FP4_E2M1) {
         const int64_t groups = a.n_tok * ((a.hkv + kHeadsPerLane - 1) / kHeadsPerLane);
-        append_gqa_fp4_kernel<<<blocks_for(groups * (a.dk / 8), 256), 256, 0, s>>>(a);
+        append_gqa_fp4_kernel<<<blocks_for(groups * (a.dk / 16), 256), 256, 0, s>>>(a);
     } else if (a.kind == DCP_GQA) {
         append_gqa_kernel<<<blocks_for(a.n_tok * a.hkv * 32, 256), 256, 0, s>>>(a);
     } else if (a.dtype == DCP_BF16) {
@@ -306,8 +332,9 @@ cudaError_t launch_gather(const AppendArgs& a, void* k_out, void* v_out, cudaStr
     if (a.n_tok == 0) return cudaSuccess;
     if (a.kind == DCP_GQA) {
         const int64_t groups = a.n_tok * ((a.hkv + kHeadsPerLane - 1) / kHeadsPerLane);
-        gather_gqa_kernel<<<blocks_for(groups * (a.dk / 8), 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out),
-                                                                              static_cast<uint8_t*>(v_out));
+        (a.dtype == DCP_FP4_E2M1 ? gather_gqa_kernel<true> : gather_gqa_kernel<false>)
+            <<<blocks_for(groups * (a.dk / 16), 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out),
+                                                                   static_cast<uint8_t*>(v_out));
     } else {
         gather_mla_kernel<<<blocks_for(a.n_tok * 32, 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out));
     }

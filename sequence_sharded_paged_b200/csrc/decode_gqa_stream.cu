@@ -270,10 +270,12 @@ __device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
 
 // A group: byte offset of its first row's codes in the pools (4-bit) or its index
 // page * hkv + head (bf16), -1: no page; first local token; shard.
-struct __align__(16) Desc {
+struct __align__(8) Desc {
     int64_t off;
     int t0;
     int shard;
+    uint32_t live;  // bit t: some row sees token t (of all 16 when every row sees the whole group)
+    uint32_t unused;
 };
 
 __device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
@@ -393,17 +395,12 @@ struct Warp {
     // copied if any query token sees it, and is zeros otherwise.  Its scales come in
     // words of four tokens; those of tokens that are not copied are cleared by the
     // reader (`keep`).
-    __device__ __forceinline__ static void copy_masked(const StreamArgs& a, const Places& from, const Desc& d, int L,
-                                                       uint32_t slot) {
+    __device__ __forceinline__ static void copy_masked(const Places& from, const Desc& d, uint32_t slot) {
         bool live[6];  // K tiles' tokens, V's four tokens
         const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        const int first = L - a.q_len;
-#pragma unroll
-        for (int e = 0; e < 6; e++) {
-            const int64_t p =
-                position_of(a, d.shard, d.t0 + (e < 2 ? 4 * (n >> 1) + (n & 1) + 2 * e : 4 * c + e - 2));
-            live[e] = d.off >= 0 && p < L && (p < a.sinks || first - p < a.window);
-        }
+        const uint32_t k = d.live >> (4 * (n >> 1) + (n & 1)), v = d.live >> (4 * c);
+        live[0] = k & 1, live[1] = k & 4;
+        live[2] = v & 1, live[3] = v & 2, live[4] = v & 4, live[5] = v & 8;
         Desc at = d;
         if (d.off < 0) at.off = at.t0 = 0;  // no page: zeros, and block 0's scales (not used)
         copy<true>(from, at, live, slot);
@@ -543,26 +540,31 @@ struct Warp {
     // Masks of a step that not every row sees all of: scores of what a row does not
     // see become -inf; of tokens that no row sees, keep[g] clears the scales (4-bit) and
     // the values are set to zero in the stage (bf16: each thread's own chunks).
-    __device__ __forceinline__ void mask(const StreamArgs& a, const Desc* d, int L, uint8_t* stage, float (*x)[4],
+    __device__ __forceinline__ void mask(const StreamArgs& a, const Desc* d, uint8_t* stage, float (*x)[4],
                                          uint32_t* keep) {
-        const int c = threadIdx.x & 3, first = L - a.q_len;
+        const int c = threadIdx.x & 3;
 #pragma unroll
         for (int g = 0; g < G; g++) {
             keep[g] = 0;
-            const bool page = d[g].off >= 0;
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const int64_t p = position_of(a, d[g].shard, d[g].t0 + token_of(c, e));
-                if (page && p < L && (p < a.sinks || first - p < a.window)) {
+                const bool live = d[g].live >> token_of(c, e) & 1;
+                if (live) {
                     keep[g] |= 0xffu << (8 * e);
                 } else if (!FP4) {
 #pragma unroll
                     for (int w = 0; w < NT / 8; w++)
                         *reinterpret_cast<uint4*>(stage + v_place(e, w)) = make_uint4(0u, 0u, 0u, 0u);
                 }
+                bool row[2] = {live, live};
+                if (a.q_len > 1 && live) {  // the rows' query tokens see different ends
+                    const int64_t p = position_of(a, d[g].shard, d[g].t0 + token_of(c, e));
+                    row[0] = sees(a, p, at[0]);
+                    row[1] = sees(a, p, at[1]);
+                }
 #pragma unroll
                 for (int h = 0; h < H; h++)
-                    if (!page || !sees(a, p, at[h])) x[2 * g + (e >> 1)][2 * h + (e & 1)] = -INFINITY;
+                    if (!row[h]) x[2 * g + (e >> 1)][2 * h + (e & 1)] = -INFINITY;
             }
         }
         if (!FP4) fence_async();  // before the stage's next copy
@@ -904,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
             const int k = 32 * kb + lane;
-            Desc d{-1, 0, 0};
+            Desc d{-1, 0, 0, 0, 0};
             bool whole_group = false;
             int i = i0 + wt + a.team * k;
             if (k < nk && i < real) {
@@ -927,10 +929,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
                 else
                     d.off = ((int64_t)pg * a.hkv + g) * (FP4 ? fp4_block_bytes(P, D) : 1) +
                             (FP4 ? (d.t0 & (P - 1)) * (D / 2) : 0);
-                const int64_t p0 = position_of(a, n, d.t0), p1 = position_of(a, n, d.t0 + kTok - 1);
-                const bool full = pg >= 0 && p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p0 < a.window);
                 d.shard = n;
-                whole_group = full;
+                if (d.off >= 0) {
+                    int64_t p = position_of(a, n, d.t0);
+                    const int64_t p1 = position_of(a, n, d.t0 + kTok - 1);
+                    whole_group = p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p < a.window);
+                    uint32_t r = (uint32_t)d.t0 % (uint32_t)a.interleave;
+                    for (int e = 0; e < kTok; e++) {
+                        if (p < L && (p < a.sinks || v.first - p < a.window)) d.live |= 1u << e;
+                        p++;
+                        if (++r == (uint32_t)a.interleave) {  // on to the shard's next run of positions
+                            r = 0;
+                            p += (int64_t)a.in - a.interleave;
+                        }
+                    }
+                }
             }
             const uint32_t mask = __ballot_sync(0xffffffffu, whole_group);
             if (kb & 1)
@@ -969,7 +982,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
                 issued++;
                 return;
             }
-            if (step_full(k)) {
+            if (k >= nk) {
+            } else if (step_full(k)) {
                 const bool live[6] = {true, true, true, true, true, true};
 #pragma unroll
                 for (int e = 0; e < C::kStep; e++)
@@ -977,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             } else {
 #pragma unroll 1
                 for (int e = 0; e < C::kStep; e++)
-                    W::copy_masked(a, places, d[e], L, ring_u32 + (slot + e) * C::kStage);
+                    W::copy_masked(places, d[e], ring_u32 + (slot + e) * C::kStage);
             }
             cp_commit();
         };
@@ -1017,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
 #pragma unroll
             for (int e = 0; e < C::kStep; e++) keep[e] = 0xffffffffu;
             const bool full = step_full(k);
-            if (!full) st.mask(a, d, L, at, x, keep);
+            if (!full) st.mask(a, d, at, x, keep);
             st.softmax(x, hi, lo);
             bool safe = true;
             if (!full && a.q_len > 1) {
@@ -1263,8 +1277,9 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         p.whole = 0;
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
-    p.lead = p.team == 1 ? 2 : 8;
-    if (getenv("ST_TEAM") && !p.whole) p.team = atoi(getenv("ST_TEAM"));
+    p.lead = p.team == 1 ? 8 : 32;
+    if (getenv("ST_WHOLE")) {p.whole=atoi(getenv("ST_WHOLE")); if(!p.whole) p.team = 2 * segs >= warps ? 1 : kWarps;}
+    if (getenv("ST_TEAM")) p.team = atoi(getenv("ST_TEAM"));
     if (getenv("ST_LEAD")) p.lead = atoi(getenv("ST_LEAD"));
     int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
     if (grid > ctas) grid = ctas;

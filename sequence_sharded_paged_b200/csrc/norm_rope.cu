@@ -11,12 +11,18 @@
 // drops the whole turns), and its upper 32 bits, as a signed fraction of a turn,
 // are within 2^-33 turns of it.
 //
-// Bound by HBM: every row is read once and written once, 4 D bytes.  Rows are 16
-// bytes a lane (D/8 lanes a row), the mean and the pairs' exchange are shuffles
-// within those lanes, and cosine and sine are computed once for each token and
-// pair, shared by all heads through shared memory.  Where they are placed follows
-// "Efficient Decode Context Parallelism with vLLM for Long Context Workloads",
-// section 4 (a position's row lies on its owner).
+// Bound by HBM: every row is read once and written once, 4 D bytes, so what has to be
+// kept down are the instructions for each row.  A row is D/8 lanes of 8 dimensions.
+// With the HALF layout a rotated lane holds dimensions 4 i .. 4 i + 3 and their
+// partners rot_dim/2 further, so that neither layout exchanges anything between lanes;
+// the mean is a shuffle sum.  Cosine and sine are computed once for each token and
+// pair and shared by all heads through shared memory; a block takes up to 8 tokens, so
+// that positions, tables and angles are looked up side by side.  Rows of a 4-bit cache
+// need 16 consecutive dimensions in two neighbouring lanes instead (one scale), and
+// exchange the pairs by shuffles.
+//
+// Where rows are placed follows "Efficient Decode Context Parallelism with vLLM for
+// Long Context Workloads", section 4 (a position's row lies on its owner).
 #include "common.cuh"
 #include "kernels.h"
 #include "rows.cuh"
@@ -38,7 +44,14 @@ __device__ __forceinline__ float2 cos_sin(const dcp_rope& rope, int p, int i) {
     return make_float2(c * rope.attn_factor, s * rope.attn_factor);
 }
 
-// Rotate this lane's 8 values.  Lanes [0, 2h) of the row hold the rot_dim = 16 h
+// One pair: (a, z) turned by the angle of c, s.
+__device__ __forceinline__ void turn(float& a, float& z, float c, float s) {
+    const float t = fmaf(a, c, -(z * s));
+    z = fmaf(z, c, a * s);
+    a = t;
+}
+
+// Rotate this lane's 8 consecutive values.  Lanes [0, 2h) of the row hold the rot_dim = 16 h
 // rotated dimensions (li counts from the first of them); `cs` are the token's
 // pairs.  HALF: the partner of dimension d is d +- rot_dim/2, in lane li +- h.
 __device__ __forceinline__ void rotate8(float* x, const float2* cs, int layout, int h, int li, int base_lane,
@@ -64,11 +77,8 @@ __device__ __forceinline__ void rotate8(float* x, const float2* cs, int layout, 
 #pragma unroll
         for (int e = 0; e < 2; e++) {
             const float4 c = c4[e];
-            const float a0 = x[4 * e], z0 = x[4 * e + 1], a1 = x[4 * e + 2], z1 = x[4 * e + 3];
-            x[4 * e] = fmaf(a0, c.x, -(z0 * c.y));
-            x[4 * e + 1] = fmaf(z0, c.x, a0 * c.y);
-            x[4 * e + 2] = fmaf(a1, c.z, -(z1 * c.w));
-            x[4 * e + 3] = fmaf(z1, c.z, a1 * c.w);
+            turn(x[4 * e], x[4 * e + 1], c.x, c.y);
+            turn(x[4 * e + 2], x[4 * e + 3], c.z, c.w);
         }
     }
 }
@@ -97,8 +107,9 @@ __device__ __forceinline__ Target find_target(const AppendArgs& a, int64_t i) {
     return t;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeArgs n,
+// FP4: the cache is a 4-bit one.
+template <int D, bool FP4>
+__global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_constant__ NormRopeArgs n,
                                                                  const __grid_constant__ dcp_rope rope) {
     constexpr int LPR = D / 8;             // lanes per row
     constexpr int GROUPS = kThreads / LPR;  // rows in flight
@@ -109,9 +120,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
     const int nt = (int)min((int64_t)n.tokens, a.n_tok - i0);
     const int lane = threadIdx.x & 31, li = lane % LPR, base_lane = lane - li;
     const int grp = threadIdx.x / LPR;
-    const uint32_t mask = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u)) << base_lane;
+    const uint32_t mask = ((1u << LPR) - 1u) << base_lane;
     const int nq = n.q ? n.hq : 0, nk = a.k_new ? a.hkv : 0;
     const int rows = nq + 2 * nk;  // queries, keys, values of one token
+
+    // this lane's dimensions: o0 .. o0 + 3 and o1 .. o1 + 3
+    const int rot_lanes = n.rotate ? rope.rot_dim / 8 : 0;
+    const bool turns = li < rot_lanes, half = rope.layout == DCP_ROPE_HALF;
+    const bool apart = !FP4 && turns && half;
+    const int o0 = apart ? 4 * li : 8 * li, o1 = apart ? rope.rot_dim / 2 + 4 * li : 8 * li + 4;
 
     // rows are numbered token by token; a group steps GROUPS rows at a time
     struct At {
@@ -124,13 +141,30 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
             p.t++;
         }
     };
-    auto load = [&](const At& p) -> uint4 {
-        const int h = p.h;
+    auto load = [&](const uint8_t* row) -> uint4 {  // not read-only loads: q_out may be q
+        const uint2 x = *reinterpret_cast<const uint2*>(row + o0 * 2), y = *reinterpret_cast<const uint2*>(row + o1 * 2);
+        return make_uint4(x.x, x.y, y.x, y.y);
+    };
+    auto source = [&](const At& p) -> const uint8_t* {
         const int64_t i = i0 + p.t;
-        const uint8_t* src = h < nq ? n.q + (i * n.q_stride + (int64_t)h * D) * 2
-                             : h < nq + nk ? a.k_new + (i * n.k_stride + (int64_t)(h - nq) * D) * 2
-                                           : a.v_new + (i * n.v_stride + (int64_t)(h - nq - nk) * D) * 2;
-        return *(reinterpret_cast<const uint4*>(src) + li);  // q_out may be q: not a read-only load
+        const uint8_t* base = n.q;
+        int64_t at = i * n.q_stride;
+        int h = p.h;
+        if (h >= nq) {
+            h -= nq;
+            base = a.k_new;
+            at = i * n.k_stride;
+            if (h >= nk) {
+                h -= nk;
+                base = a.v_new;
+                at = i * n.v_stride;
+            }
+        }
+        return base + (at + h * D) * 2;
+    };
+    auto store = [&](uint8_t* row, const uint4& w) {
+        *reinterpret_cast<uint2*>(row + o0 * 2) = make_uint2(w.x, w.y);
+        *reinterpret_cast<uint2*>(row + o1 * 2) = make_uint2(w.z, w.w);
     };
     // the first rows' loads overlap the positions', tables' and angles' work
     uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
@@ -138,11 +172,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
     next(p0);
     p1 = p0;
     next(p1);
-    if (p0.t < nt) w0 = load(p0);
-    if (p1.t < nt) w1 = load(p1);
-    uint4 qw = w0, kw = w0;
-    if (n.q_weight) qw = __ldg(reinterpret_cast<const uint4*>(n.q_weight) + li);
-    if (n.k_weight) kw = __ldg(reinterpret_cast<const uint4*>(n.k_weight) + li);
+    if (p0.t < nt) w0 = load(source(p0));
+    if (p1.t < nt) w1 = load(source(p1));
+    uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
+    if (n.q_weight) qw = load(n.q_weight);
+    if (n.k_weight) kw = load(n.k_weight);
 
     const int pairs = rope.rot_dim / 2;
     if (n.rotate)
@@ -156,50 +190,70 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const NormRopeA
         if (nk && t.pg == -1) record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
     }
     __syncthreads();
-    const float fk = a.kv_scales && nk ? __ldg(a.kv_scales) : 1.f, fv = a.kv_scales && nk ? __ldg(a.kv_scales + 1) : 1.f;
+    const float fk = FP4 && a.kv_scales && nk ? __ldg(a.kv_scales) : 1.f;
+    const float fv = FP4 && a.kv_scales && nk ? __ldg(a.kv_scales + 1) : 1.f;
 
-    auto process = [&](const At& p, const uint4& w) {
+    auto process = [&](const At& p, uint4 w) {
         const int t = p.t, h = p.h;
         const Target tg = s_target[t];
-        if (h >= nq + nk) {
-            if (tg.pg >= 0) store_gqa8(a, a.v_pages, tg.pg, h - nq - nk, tg.off, li, w, fv, mask, true);
-            return;
-        }
         const bool is_q = h < nq;
-        const uint8_t* weight = is_q ? n.q_weight : n.k_weight;
-        uint4 y = w;
-        if (weight || n.rotate) {  // otherwise the row goes through bit for bit
-            float x[8];
-            unpack8(w, x);
-            if (weight) {
-                float ss = 0.f;
+        if (h < nq + nk) {
+            const bool weight = is_q ? n.q_weight != nullptr : n.k_weight != nullptr;
+            if (weight || rot_lanes) {  // otherwise the row goes through bit for bit
+                float x[8];
+                unpack8(w, x);
+                if (weight) {
+                    float ss = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+                    for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                const float inv = rsqrtf(ss * (1.f / D) + n.eps);
-                float wt[8];
-                unpack8(is_q ? qw : kw, wt);
+                    for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+                    const float inv = rsqrtf(fmaf(ss, 1.f / D, n.eps));
+                    float wt[8];
+                    unpack8(is_q ? qw : kw, wt);
 #pragma unroll
-                for (int e = 0; e < 8; e++) x[e] = x[e] * inv * wt[e];
+                    for (int e = 0; e < 8; e++) x[e] = x[e] * inv * wt[e];
+                }
+                const float2* cs = s_cs + t * DCP_ROPE_MAX_PAIRS;
+                if (FP4) {
+                    rotate8(x, cs, rope.layout, rot_lanes / 2, li, base_lane, mask);
+                } else if (turns) {
+                    const float4* c4 = reinterpret_cast<const float4*>(cs + 4 * li);
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const float4 c = c4[e];  // pairs 2e and 2e + 1: cos, sin, cos, sin
+                        if (half) {
+                            turn(x[2 * e], x[2 * e + 4], c.x, c.y);
+                            turn(x[2 * e + 1], x[2 * e + 5], c.z, c.w);
+                        } else {
+                            turn(x[4 * e], x[4 * e + 1], c.x, c.y);
+                            turn(x[4 * e + 2], x[4 * e + 3], c.z, c.w);
+                        }
+                    }
+                }
+                w = pack8(x);
             }
-            if (n.rotate)
-                rotate8(x, s_cs + t * DCP_ROPE_MAX_PAIRS, rope.layout, rope.rot_dim / 16, li, base_lane, mask);
-            y = pack8(x);
         }
         if (is_q) {
-            if (tg.pg != -3) *(reinterpret_cast<uint4*>(n.q_out + ((i0 + t) * n.hq + h) * D * 2) + li) = y;
-        } else if (tg.pg >= 0) {
-            store_gqa8(a, a.k_pages, tg.pg, h - nq, tg.off, li, y, fk, mask, true);
+            if (tg.pg != -3) store(n.q_out + ((i0 + t) * n.hq + h) * (D * 2), w);
+            return;
         }
+        if (tg.pg < 0) return;
+        const bool is_k = h < nq + nk;
+        const int g = h - nq - (is_k ? 0 : nk);
+        uint8_t* pool = is_k ? a.k_pages : a.v_pages;
+        if (FP4)
+            store_gqa8(a, pool, tg.pg, g, tg.off, li, w, is_k ? fk : fv, mask, true);
+        else
+            store(pool + (((int64_t)tg.pg * a.hkv + g) * a.page_size + tg.off) * (D * 2), w);
     };
     while (p0.t < nt) {
         const uint4 c0 = w0, c1 = w1;
         const At a0 = p0, a1 = p1;
         next(p0), next(p0);
         next(p1), next(p1);
-        if (p0.t < nt) w0 = load(p0);
-        if (p1.t < nt) w1 = load(p1);
+        if (p0.t < nt) w0 = load(source(p0));
+        if (p1.t < nt) w1 = load(source(p1));
         process(a0, c0);
         if (a1.t < nt) process(a1, c1);
     }
@@ -342,10 +396,12 @@ cudaError_t launch_norm_rope_append(const AppendArgs& a, const dcp_rope* rope, c
     // is shared by all its tokens, as long as eight CTAs for each SM remain
     while (n.tokens < kMaxTokens && a.n_tok / (2 * n.tokens) >= 8 * num_sms) n.tokens *= 2;
     const int64_t blocks = (a.n_tok + n.tokens - 1) / n.tokens;
+    // queries alone go through the bf16 kernel whatever the cache
+    const bool fp4 = a.dtype == DCP_FP4_E2M1 && a.k_new;
     if (a.dk == 64)
-        norm_rope_gqa_kernel<64><<<(unsigned)blocks, kThreads, 0, s>>>(n, r);
+        (fp4 ? norm_rope_gqa_kernel<64, true> : norm_rope_gqa_kernel<64, false>)<<<(unsigned)blocks, kThreads, 0, s>>>(n, r);
     else
-        norm_rope_gqa_kernel<128><<<(unsigned)blocks, kThreads, 0, s>>>(n, r);
+        (fp4 ? norm_rope_gqa_kernel<128, true> : norm_rope_gqa_kernel<128, false>)<<<(unsigned)blocks, kThreads, 0, s>>>(n, r);
     return cudaGetLastError();
 }
 

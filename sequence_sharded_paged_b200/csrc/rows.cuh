@@ -32,11 +32,11 @@ __device__ __forceinline__ int append_target(const AppendArgs& a, int64_t i, int
         r = 0;  // the rank's tables are row 0
     }
     const uint32_t l = round * (uint32_t)a.interleave + ((uint32_t)p - q * (uint32_t)a.interleave);
-    const int j = (int)(l / (uint32_t)a.page_size);
+    const int j = (int)(l >> (a.page_size == 16 ? 4 : 6));  // pages are 16 or 64 tokens
     if (j >= a.max_local_pages) return -1;
     int pg = a.block_tables[((int64_t)r * a.batch + b) * a.max_local_pages + j];
     if (pg < 0 || pg >= a.num_pages) return -1;
-    *off = (int)(l % (uint32_t)a.page_size);
+    *off = (int)(l & (uint32_t)(a.page_size - 1));
     return pg;
 }
 
@@ -55,33 +55,43 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* x) {
     }
 }
 
-// Quantise a run of 16 bf16 values held by two neighbouring lanes, 8 each: returns
-// this lane's 8 codes and the run's e4m3 scale byte.  factor > 0 multiplies every
-// scale.  `both` is the mask of the lanes that take part (whole pairs).  The codes
-// are taken against the scale as rounded, so an element may lie past 6 and
-// saturates there.
+// Scale byte of a run whose largest magnitude is the larger half of am2 (bf16x2, a NaN
+// wins): e4m3(amax / (6 factor)), and the scale's value times the factor.
 //
-// x / s without a division, for factor 1: x has 8 significant bits and a border
-// between two codes, times s, at most 7, so that x / s either IS the border or is
-// 2^-15 away from it, relatively.  x * (1 / s) is within 2^-22; rounding it to 18
-// bits puts it back on the border exactly when x / s is there, and the conversion
-// then takes the even code.
-__device__ __forceinline__ uint32_t fp4_quantise8(const uint4& v, float factor, uint32_t both, uint8_t* scale_byte) {
-    constexpr uint32_t kAbs = 0x7fff7fffu;
-    uint32_t am2 = max2_nan(max2_nan(v.x & kAbs, v.y & kAbs), max2_nan(v.z & kAbs, v.w & kAbs));
-    am2 = max2_nan(am2, __shfl_xor_sync(both, am2, 1));
-    am2 = max2_nan(am2, am2 >> 16);
-    const uint8_t sb = __nv_cvt_float_to_fp8(__fdiv_rn(bf16_lo(am2), 6.f * factor), __NV_SATFINITE, __NV_E4M3);
+// Divisions by the scale (and by 6) are products with the reciprocal, for factor 1:
+// the dividend has 8 significant bits and a border between two codes, times the
+// divisor, at most 7, so that the quotient either IS the border or is 2^-15 away from
+// it, relatively.  The product is within 2^-22 of the quotient; rounding it to 18 bits
+// (snap) puts it back on the border exactly when the quotient is there, and the
+// conversion then takes the even code.
+__device__ __forceinline__ float snap(float x) { return __uint_as_float((__float_as_uint(x) + 0x20u) & ~0x3fu); }
+
+__device__ __forceinline__ uint8_t fp4_scale(uint32_t am2, float factor, float* scale) {
+    const float amax = bf16_lo(max2_nan(am2, am2 >> 16));
+    // an infinity or NaN passes through neither the reciprocal nor the rounding
+    const float q = factor == 1.f && amax < 1e38f ? snap(amax * (1.f / 6.f)) : __fdiv_rn(amax, 6.f * factor);
+    const uint8_t sb = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
     const __half_raw hr = __nv_cvt_fp8_to_halfraw(sb, __NV_E4M3);
-    const float s = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
+    *scale = __half2float(*reinterpret_cast<const __half*>(&hr)) * factor;
+    return sb;
+}
+
+__device__ __forceinline__ uint32_t fp4_abs_max(const uint4& v) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    return max2_nan(max2_nan(v.x & kAbs, v.y & kAbs), max2_nan(v.z & kAbs, v.w & kAbs));
+}
+
+// Codes of 8 bf16 values against a scale (zero or NaN: zero codes).  The scale is the
+// rounded one, so a value may lie past 6 and saturates there.
+__device__ __forceinline__ uint32_t fp4_codes8(const uint4& v, float s, float factor) {
     uint32_t w = 0;
-    if (s > 0.f) {  // false for 0 and NaN: zero codes
+    if (s > 0.f) {
         float x[8];
         unpack8(v, x);
         if (factor == 1.f) {
             const float inv = __frcp_rn(s);
 #pragma unroll
-            for (int e = 0; e < 8; e++) x[e] = __uint_as_float((__float_as_uint(x[e] * inv) + 0x20u) & ~0x3fu);
+            for (int e = 0; e < 8; e++) x[e] = snap(x[e] * inv);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; e++) x[e] = __fdiv_rn(x[e], s);
@@ -91,8 +101,18 @@ __device__ __forceinline__ uint32_t fp4_quantise8(const uint4& v, float factor, 
             w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e], x[2 * e + 1]), __NV_E2M1, cudaRoundNearest)
                  << (8 * e);
     }
-    *scale_byte = sb;
     return w;
+}
+
+// Quantise a run of 16 bf16 values held by two neighbouring lanes, 8 each: returns
+// this lane's 8 codes and the run's scale byte.  `both` is the mask of the lanes that
+// take part (whole pairs).
+__device__ __forceinline__ uint32_t fp4_quantise8(const uint4& v, float factor, uint32_t both, uint8_t* scale_byte) {
+    uint32_t am2 = fp4_abs_max(v);
+    am2 = max2_nan(am2, __shfl_xor_sync(both, am2, 1));
+    float s;
+    *scale_byte = fp4_scale(am2, factor, &s);
+    return fp4_codes8(v, s, factor);
 }
 
 // Codes of 8 values of an fp8 row whose largest magnitude is amax > 0.
