@@ -42,7 +42,6 @@
 // weights stay above fp16's smallest step.  With at most 8 query rows the two terms
 // share one instruction (rows 0..7 and 8..15 of the tile); with more they take two.
 #include <limits.h>
-#include <stdlib.h>
 
 #include "common.cuh"
 #include "finish.cuh"
@@ -241,9 +240,10 @@ struct Visible {
         *w1 = (ch.of(off, I) + kTok - 1) / kTok;
         *sg = *w0 = 0;
         if (ends) {
+            const int lo = cl.of(off, I), hi = ch.of(off, I);
             *sg = (cs.of(off, I) + kTok - 1) / kTok;
-            *w0 = max(cl.of(off, I) / kTok, *sg);
-            *w1 = max(*w0, *w1);
+            *w0 = max(lo / kTok, *sg);
+            *w1 = lo == hi ? *w0 : max(*w0, *w1);  // a shard may own none of the window: nothing of it is read
         }
     }
     // all groups of shards [lo, hi)
@@ -1278,9 +1278,6 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
     p.lead = p.team == 1 ? 8 : 32;
-    if (getenv("ST_WHOLE")) {p.whole=atoi(getenv("ST_WHOLE")); if(!p.whole) p.team = 2 * segs >= warps ? 1 : kWarps;}
-    if (getenv("ST_TEAM")) p.team = atoi(getenv("ST_TEAM"));
-    if (getenv("ST_LEAD")) p.lead = atoi(getenv("ST_LEAD"));
     int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
     if (grid > ctas) grid = ctas;
     p.ctas = (int)grid;
