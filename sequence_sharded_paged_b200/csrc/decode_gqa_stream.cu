@@ -41,13 +41,10 @@
 // range; P in two fp16 terms, with the reference 2^7 below the maximum so that small
 // weights stay above fp16's smallest step.  With at most 8 query rows the two terms
 // share one instruction (rows 0..7 and 8..15 of the tile); with more they take two.
-#include <limits.h>
-
 #include "common.cuh"
 #include "finish.cuh"
 #include "kernels.h"
-#include "rows.cuh"
-#include "tma.h"
+#include "stream.cuh"
 
 namespace dcp {
 
@@ -56,9 +53,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 2;  // by registers and by the queues' sizes
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 16;     // tokens per group
 constexpr int kDescs = 64;   // group descriptors per warp (two batches of 32)
-constexpr float kLazy = 8.f; // lazy rescale threshold (log2)
 
 // Launch constants of one cache type and head size.
 //   bf16: K and V of 16 tokens, each [D/64 halves][16 tokens][128 B] with 128-byte swizzle
@@ -75,34 +70,6 @@ struct Lane {
     static constexpr int kStep = FP4 ? 2 : 1;
     static constexpr int kSteps = FP4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // steps in the queue
     static constexpr int kStages = kStep * kSteps;
-};
-
-struct StreamArgs {
-    alignas(64) CUtensorMap map_k, map_v;  // bf16: 4-D maps of the pools, boxes of one group
-    const uint8_t* k_pages;
-    const uint8_t* v_pages;
-    const float* factors;  // 4-bit: {K, V} factors, or null
-    const int32_t* block_tables;
-    const __nv_bfloat16* q;
-    const int32_t* seq_lens;
-    float* out;
-    float* lse;
-    float* part_o;    // [2 * workers][16][D]
-    float* part_lse;  // [2 * workers][16], log2
-    int4* tail;       // [workers]: segment that starts in the worker's share and ends in another's
-    int* status;
-    int64_t* finish_ns;
-    const int64_t* t_start;
-    uint32_t in;  // interleave * n_shards, saturated
-    int32_t n_shards, interleave, page_size, num_pages, batch, max_local_pages;
-    int32_t hq, hkv, q_len, group, rows, tiles;
-    int32_t window, sinks;
-    int32_t shard_lo, shard_hi, per_shard, bt_shard0;
-    int32_t team;     // warps per team: 1 or kWarps
-    int32_t workers;  // teams in the grid
-    int32_t whole;    // whole segments, else equal shares
-    int32_t lead;     // what a segment costs beside its groups, in groups (shares count it)
-    float scale_log2;
 };
 
 // copies of this thread's own bytes; a masked copy that is not live writes zeros
@@ -161,27 +128,6 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
     mma<FP4>(d, a0, a1, a2, a3, b0, b1, d);
 }
 
-// the four bytes of w, two e2m1 values each, as four f16x2
-__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t* h) {
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t w) {  // low two bytes -> f16x2, exact
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-
 // x ~ hi + lo, two values, in the operand type
 template <bool FP4>
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
@@ -198,93 +144,6 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
         hi = *reinterpret_cast<const uint32_t*>(&h);
         lo = *reinterpret_cast<const uint32_t*>(&l);
     }
-}
-
-// positions p < x that a shard owns; `off` is the shard's first position in a round,
-// n * interleave (saturated, like a.in)
-struct Counter {
-    uint32_t base, rest;
-    __device__ __forceinline__ Counter(uint32_t x, const StreamArgs& a) {
-        const uint32_t q = x / a.in;
-        base = q * (uint32_t)a.interleave;
-        rest = x - q * a.in;
-    }
-    __device__ __forceinline__ int of(uint32_t off, uint32_t interleave) const {
-        return (int)(base + min(rest - min(rest, off), interleave));
-    }
-};
-
-__device__ __forceinline__ uint32_t round_offset(const StreamArgs& a, int n) {
-    const uint64_t off = (uint64_t)(uint32_t)n * (uint32_t)a.interleave;
-    return off > 0xffffffffu ? 0xffffffffu : (uint32_t)off;
-}
-
-// What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
-// when the two meet).
-struct Visible {
-    int L, first;  // length, position of query token 0 (may be negative)
-    bool ends;     // sinks and window apart
-    Counter cs, cl, ch;
-    __device__ __forceinline__ Visible(int len, const StreamArgs& a)
-        : L(len), first(len - a.q_len), ends(false), cs(0, a), cl(0, a), ch((uint32_t)len, a) {
-        const int lo = a.window > first ? 0 : first - a.window + 1;
-        if (lo > a.sinks) {
-            ends = true;
-            cs = Counter((uint32_t)a.sinks, a);
-            cl = Counter((uint32_t)lo, a);
-        }
-    }
-    // groups of the shard at `off`: [0, sg) and [w0, w1)
-    __device__ __forceinline__ void groups(uint32_t off, const StreamArgs& a, int* sg, int* w0, int* w1) const {
-        const uint32_t I = (uint32_t)a.interleave;
-        *w1 = (ch.of(off, I) + kTok - 1) / kTok;
-        *sg = *w0 = 0;
-        if (ends) {
-            const int lo = cl.of(off, I), hi = ch.of(off, I);
-            *sg = (cs.of(off, I) + kTok - 1) / kTok;
-            *w0 = max(lo / kTok, *sg);
-            *w1 = lo == hi ? *w0 : max(*w0, *w1);  // a shard may own none of the window: nothing of it is read
-        }
-    }
-    // all groups of shards [lo, hi)
-    __device__ __forceinline__ int count(int lo, int hi, const StreamArgs& a) const {
-        int g = 0;
-        for (int n = lo; n < hi; n++) {
-            int sg, w0, w1;
-            groups(round_offset(a, n), a, &sg, &w0, &w1);
-            g += sg + w1 - w0;
-        }
-        return g;
-    }
-};
-
-__device__ __forceinline__ int length_of(const StreamArgs& a, int b) { return max(0, __ldg(a.seq_lens + b)); }
-
-// groups of base (block of shards, request); at least 1, so that every row is written
-__device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
-    const int blk = a.per_shard ? base / a.batch : 0;
-    const Visible v(length_of(a, base - blk * a.batch), a);
-    const int lo = a.shard_lo + blk, hi = a.per_shard ? lo + 1 : a.shard_hi;
-    return max(v.count(lo, hi, a), 1);
-}
-
-// A group: byte offset of its first row's codes in the pools (4-bit) or its index
-// page * hkv + head (bf16), -1: no page; first local token; shard.
-struct __align__(8) Desc {
-    int64_t off;
-    int t0;
-    int shard;
-    uint32_t live;  // bit t: some row sees token t (of all 16 when every row sees the whole group)
-    uint32_t unused;
-};
-
-__device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
-    const uint32_t q = (uint32_t)t / (uint32_t)a.interleave;
-    return (int64_t)q * a.in + (int64_t)shard * a.interleave + (t - (int)(q * (uint32_t)a.interleave));
-}
-
-__device__ __forceinline__ bool sees(const StreamArgs& a, int64_t p, int at) {
-    return p <= at && (p < a.sinks || at - p < a.window);
 }
 
 // Everything a warp keeps for the segment it works on.
@@ -351,10 +210,9 @@ struct Warp {
                                  fmaxf(fabsf(bf16_lo(w[s].y)), fabsf(bf16_hi(w[s].y))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                int e = (int)(__float_as_uint(amax) >> 23) - 127;
-                e = (e > 127 || amax == 0.f) ? 0 : min(126, max(-126, e));
-                const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-                scale[h] = fabsf(a.scale_log2) * kf * __uint_as_float((uint32_t)(127 + e) << 23);
+                const float2 pw = row_power(amax);
+                const float f = pw.x;
+                scale[h] = fabsf(a.scale_log2) * kf * pw.y;
 #pragma unroll
                 for (int s = 0; s < KS; s++) {
                     const __half2 x = __floats2half2_rn(bf16_lo(w[s].x) * f, bf16_hi(w[s].x) * f);
@@ -746,19 +604,6 @@ struct Warp {
     }
 };
 
-// Where a row of a segment goes.
-struct Row {
-    float* o;
-    float* lse;
-};
-
-// Output row r of segment (base, g, tile): the caller's tensors.
-__device__ __forceinline__ Row out_row(const StreamArgs& a, int base, int g, int tile, int r, int D) {
-    const int rr = tile * 16 + r, j = rr / a.group, h = rr - j * a.group;
-    const int64_t at = ((int64_t)base * a.q_len + j) * a.hq + g * a.group + h;
-    return Row{a.out + at * D, a.lse + at};
-}
-
 // Two CTAs of four warps for each SM: what hides latency here is independent work
 // within a warp, which takes registers, more than a third CTA would.
 template <bool FP4, int D, bool HALF>
@@ -778,9 +623,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     __shared__ volatile int s_abort;
     __shared__ Desc s_desc[kWarps][kDescs];
     __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_ol[kWarps][16];
-    __shared__ long long s_scan[kWarps];
-    __shared__ int s_base[kWarps], s_off[kWarps];  // per team: where its share begins
-    __shared__ int s_sub[kWarps];
+    __shared__ ShareScratch<kWarps> s_share;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / a.team, wt = warp - team * a.team;  // team of the CTA, warp of the team
@@ -805,73 +648,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         }
         __syncthreads();
     }
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-            const int L = __ldg(a.seq_lens + b);
-            if (L < 0 || (L > 0 && L < a.q_len)) record_status(a.status, DCP_ERR_INVALID_ARG);
-        }
+    check_lengths(a);
 
-    // this worker's share: segments [seg, ..) step `workers`, or flat groups [r0, r1)
-    long long r0 = 0, r1 = 0, total = 0;
-    int active = a.workers;
-    int base = 0, sub = 0, x0 = 0;  // x0: where in the segment (its lead, then its groups)
-    if (!a.whole) {
-        // every CTA sums all bases' groups, a run of consecutive bases for each thread
-        const int each = (nb + kThreads - 1) / kThreads;
-        const int b0 = min(nb, (int)threadIdx.x * each), b1 = min(nb, b0 + each);
-        long long mine = 0;
-        int first_groups = 0;  // of base b0
-        for (int b = b0; b < b1; b++) {
-            const int g = base_groups(a, b);
-            if (b == b0) first_groups = g;
-            mine += (long long)(g + a.lead) * per_base;
-        }
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += t;
-        }
-        if (lane == 31) s_scan[warp] = incl;
-        __syncthreads();
-        for (int w = 0; w < kWarps; w++) {
-            if (w < warp) incl += s_scan[w];
-            total += s_scan[w];
-        }
-        // no share below 8 groups a warp: a partial costs about as much as those
-        const long long least = 8ll * a.team;
-        active = (int)min((long long)a.workers, (total + least - 1) / least);
-        for (int t = 0; t < teams; t++) {
-            const int w = blockIdx.x * teams + t;
-            if (w >= active) break;
-            long long at = total * w / active - (incl - mine);
-            if (at < 0 || at >= mine) continue;
-            for (int b = b0; b < b1; b++) {
-                const int g = b == b0 ? first_groups : base_groups(a, b);
-                const long long size = (long long)(g + a.lead) * per_base;
-                if (at < size) {
-                    s_base[t] = b;
-                    s_sub[t] = (int)(at / (g + a.lead));
-                    s_off[t] = (int)(at % (g + a.lead));
-                    break;
-                }
-                at -= size;
-            }
-        }
-        __syncthreads();
-        if (worker < active) {
-            r0 = total * worker / active;
-            r1 = total * (worker + 1) / active;
-            base = s_base[team];
-            sub = s_sub[team];
-            x0 = s_off[team];
-        }
-    }
+    // this worker's share: segments [worker, ..) step `workers`, or flat groups [r0, r1); no
+    // share below 8 groups a warp, a partial costs about as much as those
+    Share sh{0, 0, 0, 0, 0, 0, 0};
+    if (!a.whole) sh = find_share<kWarps>(a, nb, per_base, teams, team, 8ll * a.team, s_share);
+    int base = sh.base, sub = sh.sub, x0 = sh.x0;
     const typename W::Places places(a);
     uint32_t issued = 0, landed = 0;  // bf16: steps issued, and waited for
     uint32_t started = 0;             // lane 0: issued steps whose copies were started (all, but after a timeout)
     int4 tail = make_int4(-1, 0, 0, 0);
-    long long pos = r0;
+    long long pos = sh.r0;
     long long seg = worker;
     W st;
 
@@ -883,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    while (a.whole ? seg < (long long)nb * per_base : pos < r1) {
+    while (a.whole ? seg < (long long)nb * per_base : pos < sh.r1) {
         if (a.whole) {
             base = (int)(seg / per_base);
             sub = (int)(seg - (long long)base * per_base);
@@ -896,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         const int real = v.count(lo, hi, a);  // 0: nothing visible, one empty group
         const int ng = max(real, 1);
         // groups [i0, i0 + take) of the segment fall to this worker
-        const int x1 = a.whole ? ng : (int)min((long long)(ng + a.lead), x0 + (r1 - pos));
+        const int x1 = a.whole ? ng : (int)min((long long)(ng + a.lead), x0 + (sh.r1 - pos));
         const int i0 = a.whole ? 0 : max(0, x0 - a.lead), take = a.whole ? ng : max(0, x1 - a.lead) - i0;
         if (take > 0) {
         const int nk = wt < take ? (take - wt + a.team - 1) / a.team : 0;  // this warp's groups
@@ -905,46 +693,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         uint32_t full0 = 0, full1 = 0;
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
-            const int k = 32 * kb + lane;
+            const int k = 32 * kb + lane, i = i0 + wt + a.team * k;
             Desc d{-1, 0, 0, 0, 0};
             bool whole_group = false;
-            int i = i0 + wt + a.team * k;
-            if (k < nk && i < real) {
-                int n = lo;
-                for (; n < hi; n++) {
-                    int sg, w0, w1;
-                    v.groups(round_offset(a, n), a, &sg, &w0, &w1);
-                    if (i < sg + w1 - w0) {
-                        d.t0 = kTok * (i < sg ? i : w0 + i - sg);
-                        break;
-                    }
-                    i -= sg + w1 - w0;
-                }
-                const int P = a.page_size, j = d.t0 / P;
-                int pg = -1;
-                if (j < a.max_local_pages)
-                    pg = __ldg(a.block_tables + ((int64_t)(n - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
-                if (pg < 0 || pg >= a.num_pages)
-                    record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
-                else
-                    d.off = ((int64_t)pg * a.hkv + g) * (FP4 ? fp4_block_bytes(P, D) : 1) +
-                            (FP4 ? (d.t0 & (P - 1)) * (D / 2) : 0);
-                d.shard = n;
-                if (d.off >= 0) {
-                    int64_t p = position_of(a, n, d.t0);
-                    const int64_t p1 = position_of(a, n, d.t0 + kTok - 1);
-                    whole_group = p1 <= v.first && (p1 < a.sinks || (int64_t)L - 1 - p < a.window);
-                    uint32_t r = (uint32_t)d.t0 % (uint32_t)a.interleave;
-                    for (int e = 0; e < kTok; e++) {
-                        if (p < L && (p < a.sinks || v.first - p < a.window)) d.live |= 1u << e;
-                        p++;
-                        if (++r == (uint32_t)a.interleave) {  // on to the shard's next run of positions
-                            r = 0;
-                            p += (int64_t)a.in - a.interleave;
-                        }
-                    }
-                }
-            }
+            if (k < nk && i < real)
+                d = describe(a, v, lo, hi, b, g, i, FP4 ? fp4_block_bytes(a.page_size, D) : 0, D / 2, &whole_group);
             const uint32_t mask = __ballot_sync(0xffffffffu, whole_group);
             if (kb & 1)
                 full1 = mask;
@@ -1140,15 +893,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         }
         if (a.finish_ns && take > 0) {
             team_sync();
-            if (wt == 0 && lane == 0) {
-                const uint64_t dt = global_timer_ns() - (uint64_t)*a.t_start;
-                atomicMax(reinterpret_cast<unsigned long long*>(a.finish_ns + b), (unsigned long long)dt);
-            }
+            if (wt == 0 && lane == 0) record_finish(a, b);
         }
         if (!a.whole && starts && !ends) {
             // the worker whose share holds the segment's last group
-            const long long e = pos - x0 + a.lead + ng;  // one past it
-            tail = make_int4(base, sub, (int)((e * active + total - 1) / total) - 1, 0);
+            tail = make_int4(base, sub, last_worker(sh, pos - x0 + a.lead + ng), 0);
         }
         team_sync();  // queues and s_m are free again
         }
@@ -1182,11 +931,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ St
     const int rpc = 8 / wpr;
     const int r = blockIdx.y * rpc + warp / wpr, part = warp % wpr;
     const int g = t.y / a.tiles, tile = t.y - g * a.tiles;
-    const bool live = r < min(16, a.rows - tile * 16);
+    const bool live = r < min(a.tile_rows, a.rows - tile * a.tile_rows);
     const int K = t.z - (int)blockIdx.x + 1;  // parts
     const int nv = D / 4;
     // part k's slot: the tail of the first worker, the heads of the others
-    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * 16 + r; };
+    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * a.tile_rows + r; };
     float M = -INFINITY, ws = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
@@ -1242,56 +991,74 @@ cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_gqa_fp4_umma(const StreamArgs& a, int ctas, cudaStream_t s);  // decode_gqa_fp4.cu
+
 bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
     return (dk == 64 || dk == 128) && hq % hkv == 0 && q_len >= 1;
 }
 
-// Splitting rule.  In units of one group's work by one warp: whole segments cost
-// rounds * groups of the longest segment, equal shares cost the mean share plus the
-// scan of the lengths, the partials and a second kernel.
+// Which kernel, and whole segments or equal shares.  The rule compares, in units of one
+// group's work by a warp (a tile's by a block, for the tcgen05 kernel), whole segments --
+// rounds times the longest segment the tables and the mask allow -- with equal shares --
+// the mean share, plus the scan of the lengths, the partials and a second kernel.
 StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
                            int num_sms) {
     StreamPlan p;
     const int64_t rows = (int64_t)q_len * (c->hq / c->hkv);
-    const int64_t segs = (int64_t)(per_shard ? shards : 1) * c->batch * c->hkv * ((rows + 15) / 16);
+    p.umma = c->dtype == DCP_FP4_E2M1 && c->dk == 128 && rows > 8;
+    p.tile_rows = p.umma && rows > 16 ? 32 : 16;
+    const int64_t segs =
+        (int64_t)(per_shard ? shards : 1) * c->batch * c->hkv * ((rows + p.tile_rows - 1) / p.tile_rows);
     const int64_t span = per_shard ? 1 : shards;
-    // longest segment the tables and the mask allow; a shard's part starts and ends inside a group
+    // a shard's part starts and ends inside a group
     int64_t tokens = (int64_t)c->max_local_pages * c->page_size * shards;
     if (window != INT_MAX) {
         const int64_t seen = (int64_t)sinks + window + q_len - 1;
         if (seen < tokens) tokens = seen;
     }
     const int64_t groups = (tokens / shards + kTok - 1) / kTok * span + 2 * span;
-    const int64_t warps = (int64_t)num_sms * kCtasPerSm * kWarps, ctas = (int64_t)num_sms * kCtasPerSm;
-    const int64_t one = (segs + warps - 1) / warps * groups;
-    const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
-    const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
-    p.team = 1;
-    p.whole = 1;
-    int64_t best = one;
-    if (four < best) {
-        best = four;
+    const int64_t ctas = (int64_t)num_sms * kCtasPerSm;
+    if (p.umma) {
+        const int64_t tiles = (groups + 7) / 8;
+        const int64_t whole = (segs + ctas - 1) / ctas * (tiles + 4);
+        const int64_t share = (segs * (tiles + 4) + ctas - 1) / ctas + 8;
+        p.whole = whole <= share;
         p.team = kWarps;
+        p.lead = 32;
+        p.ctas = (int)(p.whole && segs < ctas ? segs : ctas);
+        p.workers = p.ctas;
+    } else {
+        const int64_t warps = ctas * kWarps;
+        const int64_t one = (segs + warps - 1) / warps * groups;
+        const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
+        const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
+        p.team = 1;
+        p.whole = 1;
+        int64_t best = one;
+        if (four < best) {
+            best = four;
+            p.team = kWarps;
+        }
+        if (share < best) {
+            p.whole = 0;
+            p.team = 2 * segs >= warps ? 1 : kWarps;
+        }
+        p.lead = p.team == 1 ? 8 : 32;
+        const int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
+        p.ctas = (int)(grid < ctas ? grid : ctas);
+        p.workers = p.ctas * (kWarps / p.team);
     }
-    if (share < best) {
-        p.whole = 0;
-        p.team = 2 * segs >= warps ? 1 : kWarps;
-    }
-    p.lead = p.team == 1 ? 8 : 32;
-    int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
-    if (grid > ctas) grid = ctas;
-    p.ctas = (int)grid;
-    p.workers = p.ctas * (kWarps / p.team);
     p.segs = segs;
     p.off_start = 0;
     p.off_tail = 256;
+    p.off_lse = p.off_o = 0;
     size_t o = p.off_tail;
     if (!p.whole) {
         o = align256(o + sizeof(int4) * (size_t)p.workers);
         p.off_lse = o;
-        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * 16);
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * p.tile_rows);
         p.off_o = o;
-        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * 16 * c->dk);
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * p.tile_rows * c->dk);
     }
     p.total = o;
     return p;
@@ -1330,7 +1097,8 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     a.q_len = q_len;
     a.group = c->hq / c->hkv;
     a.rows = q_len * a.group;
-    a.tiles = (a.rows + 15) / 16;
+    a.tile_rows = p.tile_rows;
+    a.tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
     a.window = window;
     a.sinks = sinks;
     a.shard_lo = shard_lo;
@@ -1360,7 +1128,9 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
                           CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    if (c->dk == 64) {
+    if (p.umma) {
+        e = launch_gqa_fp4_umma(a, p.ctas, s);
+    } else if (c->dk == 64) {
         if (fp4)
             e = half ? run<true, 64, true>(a, p.ctas, s) : run<true, 64, false>(a, p.ctas, s);
         else
@@ -1374,7 +1144,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     if (e != cudaSuccess || p.whole) return e;
     // few parts a segment: a row for each warp; many: a CTA for each row
     const int wpr = p.workers >= 8 * p.segs ? 8 : 1;
-    const int rows = a.rows < 16 ? a.rows : 16;
+    const int rows = a.rows < a.tile_rows ? a.rows : a.tile_rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
     cfg.blockDim = dim3(256);
