@@ -183,7 +183,7 @@ struct Warp {
         const int lane = threadIdx.x & 31, qr = lane >> 2, c = lane & 3;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            const int r = tile * 16 + qr + 8 * h;
+            const int r = tile * kRows + qr + 8 * h;
             const bool live = r < a.rows && !(HALF && h);
             const int j = live ? r / a.group : 0, hh = live ? r - j * a.group : 0;
             at[h] = live ? L - a.q_len + j : INT_MIN / 2;
@@ -260,7 +260,7 @@ struct Warp {
         live[0] = k & 1, live[1] = k & 4;
         live[2] = v & 1, live[3] = v & 2, live[4] = v & 4, live[5] = v & 8;
         Desc at = d;
-        if (d.off < 0) at.off = at.t0 = 0;  // no page: zeros, and block 0's scales (not used)
+        if (d.off < 0) at.off = at.sub = 0;  // no page: zeros, and block 0's scales (not used)
         copy<true>(from, at, live, slot);
     }
 
@@ -269,7 +269,7 @@ struct Warp {
         const int lane = threadIdx.x & 31;
         const int P = from.page;
         // d.off is the group's first row of codes; its scales lie this much less than a row a token further
-        const int64_t so = d.off - (d.t0 & (P - 1)) * (D / 2 - 1);
+        const int64_t so = d.off - d.sub * (D / 2 - 1);
         const uint8_t *k = from.k + d.off, *v = from.v + d.off, *ks = from.ks + so, *vs = from.vs + so;
         const uint32_t ds = slot + (C::kK + C::kV) * 32 + lane * 4;
         if (D == 128) {
@@ -416,7 +416,7 @@ struct Warp {
                 }
                 bool row[2] = {live, live};
                 if (a.q_len > 1 && live) {  // the rows' query tokens see different ends
-                    const int64_t p = position_of(a, d[g].shard, d[g].t0 + token_of(c, e));
+                    const int64_t p = position_in(a, d[g].p0, token_of(c, e));
                     row[0] = sees(a, p, at[0]);
                     row[1] = sees(a, p, at[1]);
                 }
@@ -559,7 +559,7 @@ struct Warp {
                 sees_v[h] = 0;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int64_t p = position_of(a, d.shard, d.t0 + token_of(lane & 3, 2 * h + e));
+                    const int64_t p = position_in(a, d.p0, token_of(lane & 3, 2 * h + e));
                     if (d.off >= 0 && sees(a, p, at_r)) sees_v[h] |= 0xffffu << (16 * e);
                 }
             }
@@ -612,9 +612,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     using C = Lane<FP4, D>;
     constexpr int S = C::kStages;
     constexpr int kRing = S * C::kStage;
-    constexpr int kRows = HALF ? 8 : 16;
+    constexpr int kMine = HALF ? 8 : kRows;  // rows that can be in use
     constexpr int kPitch = D + 4;  // floats a row of O in the team merge
-    static_assert(kRing >= kRows * kPitch * 4, "a warp's queue holds its O");
+    static_assert(kRing >= kMine * kPitch * 4, "a warp's queue holds its O");
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // the swizzle of the bf16 stages goes by the address: 1024-byte alignment
     uint8_t* smem = FP4 ? smem_raw
@@ -694,10 +694,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
             const int k = 32 * kb + lane, i = i0 + wt + a.team * k;
-            Desc d{-1, 0, 0, 0, 0};
+            Desc d{-1, 0, 0, 0};
             bool whole_group = false;
-            if (k < nk && i < real)
-                d = describe(a, v, lo, hi, b, g, i, FP4 ? fp4_block_bytes(a.page_size, D) : 0, D / 2, &whole_group);
+            if (k < nk && i < real) {
+                const Place at = place_of(a, v, lo, hi, i);
+                d = describe(a, v, at, page_at(a, at, b), g, FP4 ? fp4_block_bytes(a.page_size, D) : 0, D / 2,
+                             &whole_group);
+            }
             const uint32_t mask = __ballot_sync(0xffffffffu, whole_group);
             if (kb & 1)
                 full1 = mask;
@@ -723,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
                     uint8_t* stage = ring + at * C::kStage;
                     uint64_t* bar = &s_full[warp][at];
                     if (d->off >= 0) {
-                        const int row = (int)d->off, y = d->t0 & (a.page_size - 1);
+                        const int row = (int)d->off, y = d->sub;
                         mbar_arrive_expect_tx(bar, C::kStage);
                         tma_load_4d(stage, &a.map_k, 0, y, 0, row, bar);
                         tma_load_4d(stage + C::kK * 32, &a.map_v, 0, y, 0, row, bar);
@@ -816,17 +819,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         const bool starts = i0 == 0, ends = i0 + take == ng;
         const bool final_rows = starts && ends;
         const int part = 2 * worker + (starts ? 1 : 0);
-        const int rows = min(kRows, a.rows - tile * 16);
+        const int rows = min(kMine, a.rows - tile * kRows);
         const int qr = lane >> 2, c = lane & 3;
         auto put = [&](int r, int d, const float4& x) {  // 4 dimensions of row r
-            float* dst = final_rows ? out_row(a, base, g, tile, r, D).o : a.part_o + ((int64_t)part * 16 + r) * D;
+            float* dst = final_rows ? out_row(a, base, g, tile, r, D).o : a.part_o + ((int64_t)part * kRows + r) * D;
             *reinterpret_cast<float4*>(dst + d) = x;
         };
         auto put_lse = [&](int r, float lse2) {
             if (final_rows)
                 *out_row(a, base, g, tile, r, D).lse = lse2 * kLn2;
             else
-                a.part_lse[(int64_t)part * 16 + r] = lse2;
+                a.part_lse[(int64_t)part * kRows + r] = lse2;
         };
         if (a.team == 1) {
 #pragma unroll
@@ -931,11 +934,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ St
     const int rpc = 8 / wpr;
     const int r = blockIdx.y * rpc + warp / wpr, part = warp % wpr;
     const int g = t.y / a.tiles, tile = t.y - g * a.tiles;
-    const bool live = r < min(a.tile_rows, a.rows - tile * a.tile_rows);
+    const bool live = r < min(kRows, a.rows - tile * kRows);
     const int K = t.z - (int)blockIdx.x + 1;  // parts
     const int nv = D / 4;
     // part k's slot: the tail of the first worker, the heads of the others
-    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * a.tile_rows + r; };
+    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * kRows + r; };
     float M = -INFINITY, ws = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     if (live) {
@@ -991,24 +994,19 @@ cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_gqa_fp4_umma(const StreamArgs& a, int ctas, cudaStream_t s);  // decode_gqa_fp4.cu
-
 bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
     return (dk == 64 || dk == 128) && hq % hkv == 0 && q_len >= 1;
 }
 
-// Which kernel, and whole segments or equal shares.  The rule compares, in units of one
-// group's work by a warp (a tile's by a block, for the tcgen05 kernel), whole segments --
-// rounds times the longest segment the tables and the mask allow -- with equal shares --
-// the mean share, plus the scan of the lengths, the partials and a second kernel.
+// Whole segments or equal shares.  The rule compares, in units of one group's work by a
+// warp, whole segments -- rounds times the longest segment the tables and the mask
+// allow -- with equal shares: the mean share, plus the scan of the lengths, the partials
+// and a second kernel.
 StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
                            int num_sms) {
     StreamPlan p;
     const int64_t rows = (int64_t)q_len * (c->hq / c->hkv);
-    p.umma = c->dtype == DCP_FP4_E2M1 && c->dk == 128 && rows > 8;
-    p.tile_rows = p.umma && rows > 16 ? 32 : 16;
-    const int64_t segs =
-        (int64_t)(per_shard ? shards : 1) * c->batch * c->hkv * ((rows + p.tile_rows - 1) / p.tile_rows);
+    const int64_t segs = (int64_t)(per_shard ? shards : 1) * c->batch * c->hkv * ((rows + kRows - 1) / kRows);
     const int64_t span = per_shard ? 1 : shards;
     // a shard's part starts and ends inside a group
     int64_t tokens = (int64_t)c->max_local_pages * c->page_size * shards;
@@ -1017,37 +1015,25 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         if (seen < tokens) tokens = seen;
     }
     const int64_t groups = (tokens / shards + kTok - 1) / kTok * span + 2 * span;
-    const int64_t ctas = (int64_t)num_sms * kCtasPerSm;
-    if (p.umma) {
-        const int64_t tiles = (groups + 7) / 8;
-        const int64_t whole = (segs + ctas - 1) / ctas * (tiles + 4);
-        const int64_t share = (segs * (tiles + 4) + ctas - 1) / ctas + 8;
-        p.whole = whole <= share;
+    const int64_t ctas = (int64_t)num_sms * kCtasPerSm, warps = ctas * kWarps;
+    const int64_t one = (segs + warps - 1) / warps * groups;
+    const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
+    const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
+    p.team = 1;
+    p.whole = 1;
+    int64_t best = one;
+    if (four < best) {
+        best = four;
         p.team = kWarps;
-        p.lead = 32;
-        p.ctas = (int)(p.whole && segs < ctas ? segs : ctas);
-        p.workers = p.ctas;
-    } else {
-        const int64_t warps = ctas * kWarps;
-        const int64_t one = (segs + warps - 1) / warps * groups;
-        const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
-        const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
-        p.team = 1;
-        p.whole = 1;
-        int64_t best = one;
-        if (four < best) {
-            best = four;
-            p.team = kWarps;
-        }
-        if (share < best) {
-            p.whole = 0;
-            p.team = 2 * segs >= warps ? 1 : kWarps;
-        }
-        p.lead = p.team == 1 ? 8 : 32;
-        const int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
-        p.ctas = (int)(grid < ctas ? grid : ctas);
-        p.workers = p.ctas * (kWarps / p.team);
     }
+    if (share < best) {
+        p.whole = 0;
+        p.team = 2 * segs >= warps ? 1 : kWarps;
+    }
+    p.lead = p.team == 1 ? 8 : 32;
+    const int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
+    p.ctas = (int)(grid < ctas ? grid : ctas);
+    p.workers = p.ctas * (kWarps / p.team);
     p.segs = segs;
     p.off_start = 0;
     p.off_tail = 256;
@@ -1056,9 +1042,9 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
     if (!p.whole) {
         o = align256(o + sizeof(int4) * (size_t)p.workers);
         p.off_lse = o;
-        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * p.tile_rows);
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * kRows);
         p.off_o = o;
-        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * p.tile_rows * c->dk);
+        o = align256(o + sizeof(float) * (size_t)p.workers * 2 * kRows * c->dk);
     }
     p.total = o;
     return p;
@@ -1097,8 +1083,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     a.q_len = q_len;
     a.group = c->hq / c->hkv;
     a.rows = q_len * a.group;
-    a.tile_rows = p.tile_rows;
-    a.tiles = (a.rows + a.tile_rows - 1) / a.tile_rows;
+    a.tiles = (a.rows + kRows - 1) / kRows;
     a.window = window;
     a.sinks = sinks;
     a.shard_lo = shard_lo;
@@ -1128,9 +1113,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
                           CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    if (p.umma) {
-        e = launch_gqa_fp4_umma(a, p.ctas, s);
-    } else if (c->dk == 64) {
+    if (c->dk == 64) {
         if (fp4)
             e = half ? run<true, 64, true>(a, p.ctas, s) : run<true, 64, false>(a, p.ctas, s);
         else
@@ -1144,7 +1127,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     if (e != cudaSuccess || p.whole) return e;
     // few parts a segment: a row for each warp; many: a CTA for each row
     const int wpr = p.workers >= 8 * p.segs ? 8 : 1;
-    const int rows = a.rows < a.tile_rows ? a.rows : a.tile_rows;
+    const int rows = a.rows < kRows ? a.rows : kRows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
     cfg.blockDim = dim3(256);

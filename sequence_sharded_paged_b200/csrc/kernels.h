@@ -73,7 +73,6 @@ cudaError_t launch_decode_mla_fp8(const DecodeGeometry& g, const DecodeArgs& a, 
 
 // warp-streamed GQA decode (4-bit caches; sliding window with sinks)
 struct StreamPlan {
-    int umma, tile_rows;  // the tcgen05 kernel; query rows of a segment
     int team, whole;  // warps per team; whole segments or equal shares of all groups
     int lead;         // a segment's fixed cost, in groups
     int ctas, workers;

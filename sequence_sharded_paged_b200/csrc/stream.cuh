@@ -18,6 +18,7 @@
 namespace dcp {
 
 constexpr int kTok = 16;      // tokens per group
+constexpr int kRows = 16;     // query rows of a segment
 constexpr float kLazy = 8.f;  // lazy rescale threshold (log2)
 
 struct StreamArgs {
@@ -30,16 +31,15 @@ struct StreamArgs {
     const int32_t* seq_lens;
     float* out;
     float* lse;
-    float* part_o;    // [2 * workers][tile_rows][D]
-    float* part_lse;  // [2 * workers][tile_rows], log2
+    float* part_o;    // [2 * workers][kRows][D]
+    float* part_lse;  // [2 * workers][kRows], log2
     int4* tail;       // [workers]: segment that starts in the worker's share and ends in another's
     int* status;
     int64_t* finish_ns;
     const int64_t* t_start;
     uint32_t in;  // interleave * n_shards, saturated
     int32_t n_shards, interleave, page_size, num_pages, batch, max_local_pages;
-    int32_t hq, hkv, q_len, group, rows;
-    int32_t tiles, tile_rows;  // row tiles of a KV head, and their rows
+    int32_t hq, hkv, q_len, group, rows, tiles;  // tiles of kRows query rows for each KV head
     int32_t window, sinks;
     int32_t shard_lo, shard_hi, per_shard, bt_shard0;
     int32_t team;     // warps per team: 1 or kWarps
@@ -62,11 +62,6 @@ struct Counter {
         return (int)(base + min(rest - min(rest, off), interleave));
     }
 };
-
-__device__ __forceinline__ uint32_t round_offset(const StreamArgs& a, int n) {
-    const uint64_t off = (uint64_t)(uint32_t)n * (uint32_t)a.interleave;
-    return off > 0xffffffffu ? 0xffffffffu : (uint32_t)off;
-}
 
 // What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
 // when the two meet).
@@ -98,10 +93,12 @@ struct Visible {
     // all groups of shards [lo, hi)
     __device__ __forceinline__ int count(int lo, int hi, const StreamArgs& a) const {
         int g = 0;
+        uint64_t off = (uint64_t)(uint32_t)lo * (uint32_t)a.interleave;  // saturated as a.in is
         for (int n = lo; n < hi; n++) {
             int sg, w0, w1;
-            groups(round_offset(a, n), a, &sg, &w0, &w1);
+            groups(off > 0xffffffffu ? 0xffffffffu : (uint32_t)off, a, &sg, &w0, &w1);
             g += sg + w1 - w0;
+            off += (uint32_t)a.interleave;
         }
         return g;
     }
@@ -118,60 +115,79 @@ __device__ __forceinline__ int base_groups(const StreamArgs& a, int base) {
 }
 
 // A group: byte offset of its first row's codes in the pools (4-bit) or its index
-// page * hkv + head (bf16), -1: no page; first local token; shard.
-struct __align__(8) Desc {
+// page * hkv + head (bf16), -1: no page; position of its first token; which tokens some
+// row sees (all when every row sees the whole group); its first row in the page.
+struct __align__(16) Desc {
     int64_t off;
-    int t0;
-    int shard;
-    uint32_t live;  // bit t: some row sees token t (of all 16 when every row sees the whole group)
-    uint32_t unused;
+    int32_t p0;
+    uint16_t live, sub;
 };
 
-__device__ __forceinline__ int64_t position_of(const StreamArgs& a, int shard, int t) {
-    const uint32_t q = (uint32_t)t / (uint32_t)a.interleave;
-    return (int64_t)q * a.in + (int64_t)shard * a.interleave + (t - (int)(q * (uint32_t)a.interleave));
+// Position of token e of a group whose first token's is p0: one further for each token,
+// and past the other shards' runs where this shard's run ends.
+__device__ __forceinline__ int64_t position_in(const StreamArgs& a, int p0, int e) {
+    const uint32_t I = (uint32_t)a.interleave;
+    const uint32_t runs = ((uint32_t)p0 % I + (uint32_t)e) / I;
+    return (int64_t)p0 + e + (int64_t)runs * ((int64_t)a.in - I);
 }
 
 __device__ __forceinline__ bool sees(const StreamArgs& a, int64_t p, int at) {
     return p <= at && (p < a.sinks || at - p < a.window);
 }
 
-// Group i of the visible groups of shards [lo, hi) of request b, KV head g; *full:
-// every query token sees all of it.  block: bytes of a KV head's block (4-bit), or 0.
-__device__ __forceinline__ Desc describe(const StreamArgs& a, const Visible& v, int lo, int hi, int b, int g, int i,
-                                         int block, int row_bytes, bool* full) {
-    Desc d{-1, 0, 0, 0, 0};
-    int n = lo;
-    for (; n < hi; n++) {
+// Where group i of the visible groups of shards [lo, hi) lies (shard < 0: nowhere).
+struct Place {
+    int shard, t0;
+};
+__device__ __forceinline__ Place place_of(const StreamArgs& a, const Visible& v, int lo, int hi, int i) {
+    uint64_t off = (uint64_t)(uint32_t)lo * (uint32_t)a.interleave;
+    for (int n = lo; n < hi; n++) {
         int sg, w0, w1;
-        v.groups(round_offset(a, n), a, &sg, &w0, &w1);
-        if (i < sg + w1 - w0) {
-            d.t0 = kTok * (i < sg ? i : w0 + i - sg);
-            break;
-        }
+        v.groups(off > 0xffffffffu ? 0xffffffffu : (uint32_t)off, a, &sg, &w0, &w1);
+        if (i < sg + w1 - w0) return Place{n, kTok * (i < sg ? i : w0 + i - sg)};
         i -= sg + w1 - w0;
+        off += (uint32_t)a.interleave;
     }
-    const int P = a.page_size, j = d.t0 / P;
-    int pg = -1;
-    if (j < a.max_local_pages)
-        pg = __ldg(a.block_tables + ((int64_t)(n - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
-    d.shard = n;
+    return Place{-1, 0};
+}
+
+// Its block-table entry; -1 past the table.
+__device__ __forceinline__ int page_at(const StreamArgs& a, const Place& at, int b) {
+    const int j = at.t0 >> (a.page_size == 16 ? 4 : 6);
+    if (at.shard < 0 || j >= a.max_local_pages) return -1;
+    return __ldg(a.block_tables + ((int64_t)(at.shard - a.bt_shard0) * a.batch + b) * a.max_local_pages + j);
+}
+
+// Its descriptor for KV head g; *full: every query token sees all of it.  block: bytes
+// of a KV head's block (4-bit), or 0.
+__device__ __forceinline__ Desc describe(const StreamArgs& a, const Visible& v, const Place& at, int pg, int g,
+                                         int block, int row_bytes, bool* full) {
+    Desc d{-1, 0, 0, 0};
+    if (at.shard < 0) return d;
     if (pg < 0 || pg >= a.num_pages) {
         record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
         return d;
     }
+    d.sub = (uint16_t)(at.t0 & (a.page_size - 1));
     d.off = (int64_t)pg * a.hkv + g;
-    if (block) d.off = d.off * block + (d.t0 & (P - 1)) * row_bytes;
-    int64_t p = position_of(a, n, d.t0);
-    const int64_t p1 = position_of(a, n, d.t0 + kTok - 1);
+    if (block) d.off = d.off * block + d.sub * row_bytes;
+    const uint32_t I = (uint32_t)a.interleave;
+    const uint32_t q = (uint32_t)at.t0 / I;
+    uint32_t r = (uint32_t)at.t0 - q * I;
+    int64_t p = (int64_t)q * a.in + (int64_t)at.shard * I + r;
+    d.p0 = (int)p;  // a group has a token that counts, so its first one's position is below the length
+    const int64_t p1 = p + (kTok - 1) + (int64_t)((r + kTok - 1) / I) * ((int64_t)a.in - I);
     *full = p1 <= v.first && (p1 < a.sinks || (int64_t)v.L - 1 - p < a.window);
-    uint32_t r = (uint32_t)d.t0 % (uint32_t)a.interleave;
+    if (*full) {
+        d.live = 0xffffu;
+        return d;
+    }
     for (int e = 0; e < kTok; e++) {
-        if (p < v.L && (p < a.sinks || v.first - p < a.window)) d.live |= 1u << e;
+        if (p < v.L && (p < a.sinks || v.first - p < a.window)) d.live |= (uint16_t)(1u << e);
         p++;
-        if (++r == (uint32_t)a.interleave) {  // on to the shard's next run of positions
+        if (++r == I) {  // on to the shard's next run of positions
             r = 0;
-            p += (int64_t)a.in - a.interleave;
+            p += (int64_t)a.in - I;
         }
     }
     return d;
@@ -273,7 +289,7 @@ struct Row {
 
 // Output row r of segment (base, g, tile): the caller's tensors.
 __device__ __forceinline__ Row out_row(const StreamArgs& a, int base, int g, int tile, int r, int D) {
-    const int rr = tile * a.tile_rows + r, j = rr / a.group, h = rr - j * a.group;
+    const int rr = tile * kRows + r, j = rr / a.group, h = rr - j * a.group;
     const int64_t at = ((int64_t)base * a.q_len + j) * a.hq + g * a.group + h;
     return Row{a.out + at * D, a.lse + at};
 }
