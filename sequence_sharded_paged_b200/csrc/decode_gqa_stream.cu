@@ -53,6 +53,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 2;  // by registers and by the queues' sizes
 constexpr int kThreads = 32 * kWarps;
+constexpr int kAcc = 17 * 32;  // float4 of a warp's O in memory, and what belongs to it
 constexpr int kDescs = 64;   // group descriptors per warp (two batches of 32)
 
 // Launch constants of one cache type and head size.
@@ -107,6 +108,21 @@ __device__ __forceinline__ void cp_wait() {
 // orders this thread's writes to shared memory before later copies by the copy engine
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// four 8 x 8 matrices of 16-bit values, each lane giving one row's address; trans: transposed
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(const void* row, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+    if (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(smem_u32(row))
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(smem_u32(row))
+                     : "memory");
+}
+
 // d = a b + c
 template <bool FP4>
 __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -128,9 +144,9 @@ __device__ __forceinline__ void mma(float* d, uint32_t a0, uint32_t a1, uint32_t
     mma<FP4>(d, a0, a1, a2, a3, b0, b1, d);
 }
 
-// x ~ hi + lo, two values, in the operand type
+// x ~ hi + lo (4-bit: fp16) or hi + lo + last (bf16), two values: 22 and 24 bits
 template <bool FP4>
-__device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split(float x0, float x1, uint32_t& hi, uint32_t& lo, uint32_t& last) {
     if (FP4) {
         const __half2 h = __floats2half2_rn(x0, x1);
         const float2 f = __half22float2(h);
@@ -140,9 +156,13 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_
     } else {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
         const float2 f = __bfloat1622float2(h);
-        const __nv_bfloat162 l = __floats2bfloat162_rn(x0 - f.x, x1 - f.y);
+        x0 -= f.x, x1 -= f.y;
+        const __nv_bfloat162 l = __floats2bfloat162_rn(x0, x1);
+        const float2 g = __bfloat1622float2(l);
+        const __nv_bfloat162 m = __floats2bfloat162_rn(x0 - g.x, x1 - g.y);
         hi = *reinterpret_cast<const uint32_t*>(&h);
         lo = *reinterpret_cast<const uint32_t*>(&l);
+        last = *reinterpret_cast<const uint32_t*>(&m);
     }
 }
 
@@ -154,29 +174,45 @@ struct Warp {
     static constexpr int H = HALF ? 1 : 2;  // rows of this thread: qr (and qr + 8)
     using C = Lane<FP4, D>;
     static constexpr float kBias = FP4 ? 7.f : 0.f;
+    // terms of P, each the A operands of one group [row half + 2 * tile]; with HALF the
+    // first instruction takes terms 0 and 1 (in rows 8..15)
+    static constexpr int kTerms = FP4 ? 2 : 3;
+    using Terms = uint32_t[kTerms][4];
+    // independent parts of a score's sum: see scores()
+    static constexpr int kChains = FP4 && HALF ? 1 : 2;
+    // The instruction cuts its sums off where it should round.  bf16 caches: each product
+    // is added to O by an addition that rounds.  4-bit caches have no issue slots and
+    // registers to spare for that: `ol`, the sum of P by the same instruction, cancels
+    // what is common to all dimensions, and with two products a group (more than 8 rows)
+    // O also goes to memory, added there with rounding, after kFlush groups.  24 requests
+    // of 32k-128k tokens, relative error of O: 6.3e-6 without that, 4.9e-6 with it (fp32
+    // throughout: 4.1e-6).  An addition that rounds for each product: 379 us against 299.
+    static constexpr bool kExact = !FP4;
+    static constexpr int kFlush = kExact || HALF ? 0 : 256;
+    static constexpr int E = kExact ? 2 * H : 4;  // accumulators of an n-tile; HALF: rows 8..15 are the low terms'
     static constexpr uint32_t kOnes = FP4 ? 0x3c003c00u : 0x3f803f80u;
 
     uint32_t q[KS][HALF ? 2 : 4];
-    float o[NT][4];
-    float ol[4];  // sum of P by the same instruction: it cuts off what the product cuts off
+    float o[NT][E];
+    float ol[4];  // !kExact: sum of P
     float m[2], l[2], scale[2];
     int at[2];  // positions of rows qr and qr + 8
 
-    __device__ __forceinline__ void reset() {
+    __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int j = 0; j < NT; j++) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        for (int j = 0; j < NT; j++)
+#pragma unroll
+            for (int e = 0; e < E; e++) o[j][e] = 0.f;
         ol[0] = ol[1] = ol[2] = ol[3] = 0.f;
+    }
+    __device__ __forceinline__ void reset() {
+        clear();
         m[0] = m[1] = -INFINITY;
         l[0] = l[1] = 0.f;
     }
 
-    // bf16: which 16-byte chunk of a 128-byte half row thread column n holds; with the
-    // swizzle, the eight lanes of a shared-memory phase then hit eight different chunks
-    __device__ __forceinline__ static int chunk_of(int n) { return (n >> 1) | ((n & 1) << 2); }
-    // first of the 8 dimensions that thread column n holds in n-tiles 8 w .. 8 w + 7
-    __device__ __forceinline__ static int dim_of(int n, int w) { return FP4 ? n * NT + 8 * w : (chunk_of(n) + 8 * w) * 8; }
     // the four tokens that thread column c holds of P and V: x[t][e] is token_of(c, 2 t + e)
-    __device__ __forceinline__ static int token_of(int c, int i) { return FP4 ? 4 * c + i : c + 4 * i; }
+    __device__ __forceinline__ static int token_of(int c, int i) { return FP4 ? 4 * c + i : 2 * c + (i & 1) + 8 * (i >> 1); }
 
     // Q fragments of rows qr (and qr + 8) of tile `tile` of KV head g
     __device__ __forceinline__ void load_q(const StreamArgs& a, int b, int g, int tile, int L, float kf) {
@@ -194,8 +230,12 @@ struct Warp {
             uint2 w[KS];
 #pragma unroll
             for (int s = 0; s < KS; s++) {
-                const int d4 = FP4 ? (D / 4 * c) / 4 + s : (s >> 1) * 8 + c * 2 + (s & 1);
-                w[s] = live ? __ldg(src + d4) : make_uint2(0, 0);
+                w[s] = make_uint2(0, 0);
+                if (live && FP4) w[s] = __ldg(src + (D / 4 * c) / 4 + s);
+                if (live && !FP4) {
+                    const uint32_t* two = reinterpret_cast<const uint32_t*>(src) + 8 * s + c;
+                    w[s] = make_uint2(__ldg(two), __ldg(two + 4));
+                }
                 if (a.scale_log2 < 0.f) {  // the sign of the scale goes into q: scale[] >= 0
                     w[s].x ^= 0x80008000u;
                     w[s].y ^= 0x80008000u;
@@ -291,16 +331,10 @@ struct Warp {
         }
     }
 
-    // bf16: this thread's byte offsets in a stage: K, token (n >> 1) + 4 (n & 1) (+ 8 for
-    // tile 1), chunk 4 (i & 1) + c of half i / 2; V, token c + 4 e, chunk_of(n) of half w
-    __device__ __forceinline__ static int k_place(int t, int i) {
-        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        const int row = (n >> 1) + 4 * (n & 1);
-        return (i >> 1) * 2048 + (row + 8 * t) * 128 + (((c ^ row) << 4) ^ ((i & 1) << 6));
-    }
-    __device__ __forceinline__ static int v_place(int e, int w) {
-        const int lane = threadIdx.x & 31, n = lane >> 2, c = lane & 3;
-        return C::kK * 32 + w * 2048 + (c + 4 * e) * 128 + (((chunk_of(n) ^ c) << 4) ^ ((e & 1) << 6));
+    // bf16: byte offset of chunk `chunk` (8 dimensions) of a token's K or V row in a stage, as the
+    // copies' 128-byte swizzle places it
+    __device__ __forceinline__ static int row_place(int token, int chunk) {
+        return (chunk >> 3) * 2048 + token * 128 + (((chunk ^ token) & 7) << 4);
     }
 
     // V operands of n-tiles 8 w .. 8 w + 7: b[j][h] tokens token_of(c, 2h), token_of(c, 2h + 1).
@@ -308,20 +342,11 @@ struct Warp {
     __device__ __forceinline__ static void load_v(const uint8_t* slot, int w, uint32_t keep, uint32_t (*b)[2]) {
         const int lane = threadIdx.x & 31;
         if (!FP4) {
-            uint4 v[4];
+            // matrices: tokens 0..7 and 8..15 of chunk j, the same of chunk j + 1
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-                v[e] = *reinterpret_cast<const uint4*>(slot + v_place(e, w));
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t x[4] = {v[2 * h].x, v[2 * h].y, v[2 * h].z, v[2 * h].w};
-                const uint32_t y[4] = {v[2 * h + 1].x, v[2 * h + 1].y, v[2 * h + 1].z, v[2 * h + 1].w};
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    b[2 * k][h] = __byte_perm(x[k], y[k], 0x5410);
-                    b[2 * k + 1][h] = __byte_perm(x[k], y[k], 0x7632);
-                }
-            }
+            for (int j = 0; j < 8; j += 2)
+                ldmatrix4<true>(slot + C::kK * 32 + row_place(lane & 15, 8 * w + j + (lane >> 4)), b[j][0], b[j][1],
+                                b[j + 1][0], b[j + 1][1]);
         } else {
             uint32_t v[4];
 #pragma unroll
@@ -349,17 +374,21 @@ struct Warp {
     }
 
     // Scores of one group: x[t][e], e = 0, 1: row qr, token_of(c, 2t + e); e = 2, 3: row qr + 8
+    // The instruction cuts its sums off where it should round, so each tile's sum is taken
+    // in kChains independent parts, added at the end with rounding.
     __device__ __forceinline__ void scores(const uint8_t* slot, float (*x)[4]) {
         const int lane = threadIdx.x & 31, n = lane >> 2;
+        float y[2][kChains][4];
         if (!FP4) {
+            // matrices: chunks 2 s and 2 s + 1 of tokens 0..7, the same of tokens 8..15
 #pragma unroll
-            for (int i = 0; i < D / 32; i++)
+            for (int s = 0; s < KS; s++) {
+                uint32_t k[2][2];
+                ldmatrix4<false>(slot + row_place((lane & 7) + (lane >> 4) * 8, 2 * s + (lane >> 3 & 1)), k[0][0], k[0][1],
+                                 k[1][0], k[1][1]);
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    const uint4 k = *reinterpret_cast<const uint4*>(slot + k_place(t, i));
-                    qk(x[t], 2 * i, k.x, k.y);
-                    qk(x[t], 2 * i + 1, k.z, k.w);
-                }
+                for (int t = 0; t < 2; t++) qk(y[t], s, k[t][0], k[t][1]);
+            }
         } else {
 #pragma unroll
             for (int t = 0; t < 2; t++) {
@@ -380,11 +409,19 @@ struct Warp {
                     const uint32_t s = e4m3x2(__byte_perm(sw, 0, sel));
                     uint32_t h[4];
                     e2m1x8(kw[w], h);
-                    qk(x[t], 2 * w, mul2(h[0], s), mul2(h[1], s));
-                    qk(x[t], 2 * w + 1, mul2(h[2], s), mul2(h[3], s));
+                    qk(y[t], 2 * w, mul2(h[0], s), mul2(h[1], s));
+                    qk(y[t], 2 * w + 1, mul2(h[2], s), mul2(h[3], s));
                 }
             }
         }
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int e = 0; e < 2 * H; e++) {
+                x[t][e] = y[t][0][e];
+#pragma unroll
+                for (int i = 1; i < kChains; i++) x[t][e] += y[t][i][e];
+            }
     }
 
     static constexpr int G = C::kStep;
@@ -400,7 +437,7 @@ struct Warp {
     // the values are set to zero in the stage (bf16: each thread's own chunks).
     __device__ __forceinline__ void mask(const StreamArgs& a, const Desc* d, uint8_t* stage, float (*x)[4],
                                          uint32_t* keep) {
-        const int c = threadIdx.x & 3;
+        const int c = threadIdx.x & 3, n = (threadIdx.x & 31) >> 2;
 #pragma unroll
         for (int g = 0; g < G; g++) {
             keep[g] = 0;
@@ -412,7 +449,8 @@ struct Warp {
                 } else if (!FP4) {
 #pragma unroll
                     for (int w = 0; w < NT / 8; w++)
-                        *reinterpret_cast<uint4*>(stage + v_place(e, w)) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(stage + C::kK * 32 + row_place(token_of(c, e), 8 * w + n)) =
+                            make_uint4(0u, 0u, 0u, 0u);
                 }
                 bool row[2] = {live, live};
                 if (a.q_len > 1 && live) {  // the rows' query tokens see different ends
@@ -425,11 +463,14 @@ struct Warp {
                     if (!row[h]) x[2 * g + (e >> 1)][2 * h + (e & 1)] = -INFINITY;
             }
         }
-        if (!FP4) fence_async();  // before the stage's next copy
+        if (!FP4) {
+            fence_async();  // before the stage's next copy
+            __syncwarp();
+        }
     }
 
-    // One softmax step: x becomes the A operands of P V (hi + lo terms), [row half + 2 * tile].
-    __device__ __forceinline__ void softmax(const float (*x)[4], uint32_t (*hi)[4], uint32_t (*lo)[4]) {
+    // One softmax step: x becomes the terms of P.
+    __device__ __forceinline__ void softmax(const float (*x)[4], Terms* p) {
         float mx[H];
         bool grow = false;
 #pragma unroll
@@ -464,39 +505,67 @@ struct Warp {
                 const float p0 = fast_exp2(fmaf(x[t][2 * h], scale[h], -ref));
                 const float p1 = fast_exp2(fmaf(x[t][2 * h + 1], scale[h], -ref));
                 sum += p0 + p1;
-                split2<FP4>(p0, p1, hi[t >> 1][h + 2 * (t & 1)], lo[t >> 1][h + 2 * (t & 1)]);
+                const int i = h + 2 * (t & 1);
+                split<FP4>(p0, p1, p[t >> 1][0][i], p[t >> 1][1][i], p[t >> 1][kTerms - 1][i]);
             }
             l[h] += sum;
         }
-        if (HALF) {  // rows 8..15 carry the low terms
+        if (HALF) {
 #pragma unroll
             for (int g = 0; g < G; g++) {
-                hi[g][1] = lo[g][0];
-                hi[g][3] = lo[g][2];
+                p[g][0][1] = p[g][1][0];
+                p[g][0][3] = p[g][1][2];
+                if (!FP4) p[g][kTerms - 1][1] = p[g][kTerms - 1][3] = 0u;
             }
         }
     }
 
+    __device__ __forceinline__ static void mul(float* d, const uint32_t* p, uint32_t b0, uint32_t b1) {
+        mma<FP4>(d, p[0], p[1], p[2], p[3], b0, b1);
+    }
+    __device__ __forceinline__ static void first(float* d, const Terms& p, uint32_t b0, uint32_t b1) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        mma<FP4>(d, p[0][0], p[0][1], p[0][2], p[0][3], b0, b1, zero);
+    }
+    // o += t; with HALF rows 8..15 of t belong to rows 0..7
+    __device__ __forceinline__ static void add(float* o, const float* t) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) o[e % E] += t[e];
+    }
+
     // O += P V
-    __device__ __forceinline__ void values(const uint8_t* at, const uint32_t* keep, const uint32_t (*hi)[4],
-                                           const uint32_t (*lo)[4]) {
+    __device__ __forceinline__ void values(const uint8_t* at, const uint32_t* keep, const Terms* p) {
 #pragma unroll
         for (int g = 0; g < G; g++) {
 #pragma unroll
             for (int w = 0; w < NT / 8; w++) {
                 uint32_t b[8][2];
                 load_v(at + g * C::kStage, w, keep[g], b);
+                if (!kExact) {
 #pragma unroll
-                for (int j = 0; j < 8; j++)
-                    mma<FP4>(o[8 * w + j], hi[g][0], hi[g][1], hi[g][2], hi[g][3], b[j][0], b[j][1]);
-                if (!HALF) {
+                    for (int i = 0; i < (HALF ? 1 : kTerms); i++)
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        mma<FP4>(o[8 * w + j], lo[g][0], lo[g][1], lo[g][2], lo[g][3], b[j][0], b[j][1]);
+                        for (int j = 0; j < 8; j++) mul(o[8 * w + j], p[g][i], b[j][0], b[j][1]);
+                    continue;
+                }
+                constexpr int kAhead = 4;  // products in flight
+#pragma unroll
+                for (int j0 = 0; j0 < 8; j0 += kAhead) {
+                    float t[kAhead][4];
+#pragma unroll
+                    for (int j = 0; j < kAhead; j++) first(t[j], p[g], b[j0 + j][0], b[j0 + j][1]);
+#pragma unroll
+                    for (int i = HALF ? 2 : 1; i < kTerms; i++)
+#pragma unroll
+                        for (int j = 0; j < kAhead; j++) mul(t[j], p[g][i], b[j0 + j][0], b[j0 + j][1]);
+#pragma unroll
+                    for (int j = 0; j < kAhead; j++) add(o[8 * w + j0 + j], t[j]);
                 }
             }
-            mma<FP4>(ol, hi[g][0], hi[g][1], hi[g][2], hi[g][3], kOnes, kOnes);
-            if (!HALF) mma<FP4>(ol, lo[g][0], lo[g][1], lo[g][2], lo[g][3], kOnes, kOnes);
+            if (!kExact) {
+#pragma unroll
+                for (int i = 0; i < (HALF ? 1 : kTerms); i++) mul(ol, p[g][i], kOnes, kOnes);
+            }
         }
     }
 
@@ -505,9 +574,9 @@ struct Warp {
         for (int j = 0; j < NT; j++) {
             o[j][2 * h] *= f;
             o[j][2 * h + 1] *= f;
-            if (HALF) {
-                o[j][2] *= f;
-                o[j][3] *= f;
+            if (HALF && E == 4) {
+                o[j][E - 2] *= f;
+                o[j][E - 1] *= f;
             }
         }
         ol[2 * h] *= f;
@@ -518,9 +587,10 @@ struct Warp {
         }
     }
 
-    __device__ __forceinline__ void qk(float* d, int s, uint32_t b0, uint32_t b1) {
+    __device__ __forceinline__ void qk(float (*y)[4], int s, uint32_t b0, uint32_t b1) {
         const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        const float* c = s == 0 ? zero : d;
+        float* d = y[s % kChains];
+        const float* c = s < kChains ? zero : d;
         if (HALF)
             mma<FP4>(d, q[s][0], 0u, q[s][1], 0u, b0, b1, c);
         else
@@ -547,7 +617,7 @@ struct Warp {
     // O += P V of one group where some rows must not see a non-finite value that
     // others see: row by row, with the values that the row does not see set to zero.
     __device__ __forceinline__ void careful(const StreamArgs& a, const Desc& d, const uint8_t* slot, uint32_t keep,
-                                            const uint32_t* hi, const uint32_t* lo) {
+                                            const Terms& p) {
         const int lane = threadIdx.x & 31, qr = lane >> 2;
 #pragma unroll 1
         for (int r = 0; r < (HALF ? 8 : 16); r++) {
@@ -559,8 +629,8 @@ struct Warp {
                 sees_v[h] = 0;
 #pragma unroll
                 for (int e = 0; e < 2; e++) {
-                    const int64_t p = position_in(a, d.p0, token_of(lane & 3, 2 * h + e));
-                    if (d.off >= 0 && sees(a, p, at_r)) sees_v[h] |= 0xffffu << (16 * e);
+                    const int64_t x = position_in(a, d.p0, token_of(lane & 3, 2 * h + e));
+                    if (d.off >= 0 && sees(a, x, at_r)) sees_v[h] |= 0xffffu << (16 * e);
                 }
             }
 #pragma unroll
@@ -569,35 +639,92 @@ struct Warp {
                 load_v(slot, w, keep, b);
 #pragma unroll
                 for (int j = 0; j < 8; j++) {
-                    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
                     float t[4];
-                    mma<FP4>(t, hi[0], hi[1], hi[2], hi[3], b[j][0] & sees_v[0], b[j][1] & sees_v[1], zero);
-                    if (!HALF) mma<FP4>(t, lo[0], lo[1], lo[2], lo[3], b[j][0] & sees_v[0], b[j][1] & sees_v[1]);
+                    const uint32_t b0 = b[j][0] & sees_v[0], b1 = b[j][1] & sees_v[1];
+                    first(t, p, b0, b1);
+#pragma unroll
+                    for (int i = HALF ? 2 : 1; i < kTerms; i++) mul(t, p[i], b0, b1);
                     if (qr == (r & 7)) {
 #pragma unroll
                         for (int e = 0; e < 4; e++)
-                            if (HALF || (e >> 1) == (r >> 3)) o[8 * w + j][e] += t[e];
+                            if (HALF || (e >> 1) == (r >> 3)) o[8 * w + j][e % E] += t[e];
                     }
                 }
             }
         }
-        mma<FP4>(ol, hi[0], hi[1], hi[2], hi[3], kOnes, kOnes);
-        if (!HALF) mma<FP4>(ol, lo[0], lo[1], lo[2], lo[3], kOnes, kOnes);
+        if (!kExact) {
+#pragma unroll
+            for (int i = 0; i < (HALF ? 1 : kTerms); i++) mul(ol, p[i], kOnes, kOnes);
+        }
     }
 
-    // After the last group: whole-row sums, the low terms folded in, l and m the same
-    // in the row's four lanes.
+    // acc (this lane's own column) = acc + O, at the reference m, and O = 0; the last
+    // float4 holds the reference and the sums `ol`.  (!kExact)
+    __device__ __forceinline__ void flush(float4* acc, bool first) {
+        if (!first) unflush(acc);
+#pragma unroll
+        for (int j = 0; j < NT; j++) acc[j * 32] = make_float4(o[j][0], o[j][1], o[j][E - 2], o[j][E - 1]);
+        acc[kAcc - 32] = make_float4(m[0], m[1], ol[0], ol[2]);
+        clear();
+    }
+    // O = O + acc, at the reference m
+    __device__ __forceinline__ void unflush(const float4* acc) {
+        const float4 s = acc[kAcc - 32];
+        const float f0 = s.x == -INFINITY ? 0.f : fast_exp2(s.x - m[0]);
+        const float f1 = HALF ? f0 : s.y == -INFINITY ? 0.f : fast_exp2(s.y - m[1]);
+#pragma unroll
+        for (int j = 0; j < NT; j++) {
+            const float4 x = acc[j * 32];
+            o[j][0] = fmaf(f0, x.x, o[j][0]);
+            o[j][1] = fmaf(f0, x.y, o[j][1]);
+            o[j][E - 2] = fmaf(f1, x.z, o[j][E - 2]);
+            o[j][E - 1] = fmaf(f1, x.w, o[j][E - 1]);
+        }
+        ol[0] = fmaf(f0, s.z, ol[0]);
+        ol[2] = fmaf(f1, s.w, ol[2]);
+    }
+
+    // O of row qr + 8 h, four dimensions at a time: put(first dimension, values).  bf16: neighbours
+    // in c exchange pairs.  Executed by whole warps.
+    template <class F>
+    __device__ __forceinline__ void each(int h, int c, F put) const {
+        if (FP4) {
+#pragma unroll
+            for (int e = 0; e < 2; e++)
+#pragma unroll
+                for (int j = 0; j < NT; j += 4)
+                    put((2 * c + e) * NT + j, make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e],
+                                                          o[j + 3][2 * h + e]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                // the even lane takes n-tile j, the odd one n-tile j + 1
+                const bool odd = c & 1;
+                const float a0 = odd ? o[j + 1][2 * h] : o[j][2 * h], a1 = odd ? o[j + 1][2 * h + 1] : o[j][2 * h + 1];
+                float b0 = odd ? o[j][2 * h] : o[j + 1][2 * h], b1 = odd ? o[j][2 * h + 1] : o[j + 1][2 * h + 1];
+                b0 = __shfl_xor_sync(0xffffffffu, b0, 1);
+                b1 = __shfl_xor_sync(0xffffffffu, b1, 1);
+                put(8 * (j + (c & 1)) + 4 * (c >> 1), odd ? make_float4(b0, b1, a0, a1) : make_float4(a0, a1, b0, b1));
+            }
+        }
+    }
+
+    // what O is to be divided by
+    __device__ __forceinline__ float sum(int h) const { return kExact ? l[h] : ol[2 * h]; }
+
+    // After the last group: whole-row sums, the same in the row's four lanes; the low
+    // terms' rows are added in.
     __device__ __forceinline__ void close() {
 #pragma unroll
-        for (int h = 0; h < (HALF ? 1 : 2); h++) {
+        for (int h = 0; h < H; h++) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
-        if (HALF) {
+        if (HALF && E == 4) {
 #pragma unroll
             for (int j = 0; j < NT; j++) {
-                o[j][0] += o[j][2];
-                o[j][1] += o[j][3];
+                o[j][0] += o[j][E - 2];
+                o[j][1] += o[j][E - 1];
             }
             ol[0] += ol[2];
         }
@@ -656,6 +783,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     if (!a.whole) sh = find_share<kWarps>(a, nb, per_base, teams, team, 8ll * a.team, s_share);
     int base = sh.base, sub = sh.sub, x0 = sh.x0;
     const typename W::Places places(a);
+    // this lane's column of its warp's O in memory
+    auto acc = [&]() { return a.acc + ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kAcc + (threadIdx.x & 31); };
     uint32_t issued = 0, landed = 0;  // bf16: steps issued, and waited for
     uint32_t started = 0;             // lane 0: issued steps whose copies were started (all, but after a timeout)
     int4 tail = make_int4(-1, 0, 0, 0);
@@ -775,20 +904,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         float x[2 * C::kStep][4];
         uint8_t* here = arrived(0, 0);
         st.step_scores(here, x);
+        int k = 0;
 #pragma unroll 1
-        for (int k = 0; k < nk; k += C::kStep) {
+        for (;;) {
+        const int stop = W::kFlush && a.acc ? min(nk, k + W::kFlush) : nk;
+#pragma unroll 1
+        for (; k < stop; k += C::kStep) {
             start(k + (C::kSteps - 1) * C::kStep, slot_in);
             if ((slot_in += C::kStep) == S) slot_in = 0;
             uint8_t* at = here;
             if ((slot_out += C::kStep) == S) slot_out = 0;
             here = arrived(k + C::kStep, slot_out);
             const Desc* d = descs + (k & (kDescs - 1));
-            uint32_t keep[C::kStep], hi[C::kStep][4], lo[C::kStep][4];
+            uint32_t keep[C::kStep];
+            typename W::Terms p[C::kStep];
 #pragma unroll
             for (int e = 0; e < C::kStep; e++) keep[e] = 0xffffffffu;
             const bool full = step_full(k);
             if (!full) st.mask(a, d, at, x, keep);
-            st.softmax(x, hi, lo);
+            st.softmax(x, p);
             bool safe = true;
             if (!full && a.q_len > 1) {
 #pragma unroll
@@ -796,23 +930,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             }
             if (safe) {
                 st.step_scores(here, x);
-                st.values(at, keep, hi, lo);
+                st.values(at, keep, p);
             } else {
 #pragma unroll 1
                 for (int e = 0; e < C::kStep; e++) {
-                    uint32_t h[4], w[4];  // chosen without an index, so that hi and lo stay in registers
+                    typename W::Terms t;  // chosen without an index, so that p stays in registers
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        h[i] = e ? hi[C::kStep - 1][i] : hi[0][i];
-                        w[i] = e ? lo[C::kStep - 1][i] : lo[0][i];
-                    }
-                    st.careful(a, d[e], at + e * C::kStage, e ? keep[C::kStep - 1] : keep[0], h, w);
+                    for (int i = 0; i < W::kTerms * 4; i++) t[i / 4][i % 4] = e ? p[C::kStep - 1][i / 4][i % 4] : p[0][i / 4][i % 4];
+                    st.careful(a, d[e], at + e * C::kStage, e ? keep[C::kStep - 1] : keep[0], t);
                 }
                 st.step_scores(here, x);
             }
         }
+        if (k >= nk) break;
+        if (W::kFlush) st.flush(acc(), k == W::kFlush);
+        }
         cp_wait<0>();
         __syncwarp();  // the next segment's descriptors overwrite these
+        if (W::kFlush && nk > W::kFlush && a.acc) st.unflush(acc());
         st.close();
 
         // where the rows go: the caller's tensors, or a slot of the workspace
@@ -835,15 +970,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
 #pragma unroll
             for (int h = 0; h < (HALF ? 1 : 2); h++) {
                 const int r = qr + 8 * h;
+                const float inv = st.l[h] == 0.f ? 0.f : vf / st.sum(h);
+                st.each(h, c, [&](int d, const float4& x) {
+                    if (r < rows) put(r, d, make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv));
+                });
                 if (r < rows) {
-                    const float inv = st.l[h] == 0.f ? 0.f : vf / st.ol[2 * h];
-#pragma unroll
-                    for (int e = 0; e < 2; e++)
-#pragma unroll
-                        for (int j = 0; j < W::NT; j += 4)
-                            put(r, W::dim_of(2 * c + e, j / 8) + (j & 7),
-                                make_float4(st.o[j][2 * h + e] * inv, st.o[j + 1][2 * h + e] * inv,
-                                            st.o[j + 2][2 * h + e] * inv, st.o[j + 3][2 * h + e] * inv));
                     if (c == 0) put_lse(r, st.l[h] == 0.f ? -INFINITY : (st.m[h] == -INFINITY ? 0.f : st.m[h]) + log2f(st.l[h]));
                 }
             }
@@ -854,18 +985,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
 #pragma unroll
             for (int h = 0; h < (HALF ? 1 : 2); h++) {
                 const int r = qr + 8 * h;
-#pragma unroll
-                for (int e = 0; e < 2; e++)
-#pragma unroll
-                    for (int j = 0; j < W::NT; j += 4)
-                        *reinterpret_cast<float4*>(so + r * kPitch + W::dim_of(2 * c + e, j / 8) + (j & 7)) =
-                            make_float4(st.o[j][2 * h + e], st.o[j + 1][2 * h + e], st.o[j + 2][2 * h + e],
-                                        st.o[j + 3][2 * h + e]);
+                st.each(h, c, [&](int d, const float4& x) { *reinterpret_cast<float4*>(so + r * kPitch + d) = x; });
                 if (!FP4) fence_async();
                 if (c == 0) {
                     s_m[warp][r] = st.m[h];
                     s_l[warp][r] = st.l[h];
-                    s_ol[warp][r] = st.ol[2 * h];
+                    s_ol[warp][r] = st.sum(h);
                 }
             }
             __syncthreads();
@@ -1037,8 +1162,14 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
     p.segs = segs;
     p.off_start = 0;
     p.off_tail = 256;
-    p.off_lse = p.off_o = 0;
+    p.off_lse = p.off_o = p.off_acc = 0;
     size_t o = p.off_tail;
+    using W = Warp<true, 64, false>;
+    if (c->dtype == DCP_FP4_E2M1 && rows > kRows / 2 && groups > W::kFlush) {
+        p.off_acc = o;
+        o += sizeof(float4) * kAcc * (size_t)p.ctas * kWarps;
+        p.off_tail = o;
+    }
     if (!p.whole) {
         o = align256(o + sizeof(int4) * (size_t)p.workers);
         p.off_lse = o;
@@ -1066,6 +1197,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     a.lse = lse;
     a.part_o = p.whole ? nullptr : reinterpret_cast<float*>(w + p.off_o);
     a.part_lse = p.whole ? nullptr : reinterpret_cast<float*>(w + p.off_lse);
+    a.acc = p.off_acc ? reinterpret_cast<float4*>(w + p.off_acc) : nullptr;
     a.tail = p.whole ? nullptr : reinterpret_cast<int4*>(w + p.off_tail);
     a.status = status;
     a.finish_ns = finish_ns;

@@ -77,7 +77,7 @@ struct StreamPlan {
     int lead;         // a segment's fixed cost, in groups
     int ctas, workers;
     int64_t segs;
-    size_t off_start, off_tail, off_lse, off_o, total;  // workspace
+    size_t off_start, off_acc, off_tail, off_lse, off_o, total;  // workspace
 };
 bool gqa_stream_supported(int hq, int hkv, int dk, int q_len);
 // shards: how many are decoded; per_shard: a partial for each, else their sum

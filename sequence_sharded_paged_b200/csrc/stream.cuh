@@ -33,6 +33,7 @@ struct StreamArgs {
     float* lse;
     float* part_o;    // [2 * workers][kRows][D]
     float* part_lse;  // [2 * workers][kRows], log2
+    float4* acc;      // [warps][kAcc] each warp's O between two flushes, or null
     int4* tail;       // [workers]: segment that starts in the worker's share and ends in another's
     int* status;
     int64_t* finish_ns;
