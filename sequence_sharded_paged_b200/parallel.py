@@ -8,7 +8,7 @@ exp(LSE_rank - LSE), and a reduce-scatter sums the reweighted partials so that
 each GPU ends with the merged output of its share of the heads.
 
 Here the attention, the reweighting and the reduce-scatter layout run in
-libdcp (dcp_decode_rank, dcp_lse_rescale); torch.distributed carries the two
+libdcp (dcp_decode_rank or dcp_decode_window, dcp_lse_rescale); torch.distributed carries the two
 collectives (NCCL over NVLink on GPUs, gloo in the CPU tests).  This module only
 orders those calls and allocates their buffers.
 """
@@ -17,14 +17,21 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from . import DCP_DECODE_RANK, CacheDesc, dcp_decode_rank, dcp_decode_workspace_size_ex, dcp_lse_rescale
+from . import (DCP_DECODE_RANK, CacheDesc, dcp_decode_rank, dcp_decode_window, dcp_decode_window_workspace_size,
+               dcp_decode_workspace_size_ex, dcp_lse_rescale)
 
 
-def rank_workspace(desc: CacheDesc, batch: int, q_len: int = 1, device=None) -> torch.Tensor:
-    """Workspace of dcp_decode_rank for this rank's cache."""
-    n = dcp_decode_workspace_size_ex(desc, batch, q_len, DCP_DECODE_RANK)
+def rank_workspace(desc: CacheDesc, batch: int, q_len: int = 1, device=None, rank: int | None = None,
+                   window: int | None = None, n_sinks: int = 0) -> torch.Tensor:
+    """Workspace of dcp_decode_rank for this rank's cache (window: of dcp_decode_window as rank `rank`)."""
+    if window is None:
+        n = dcp_decode_workspace_size_ex(desc, batch, q_len, DCP_DECODE_RANK)
+    else:
+        if rank is None:
+            raise ValueError("a windowed decode's workspace needs the rank")
+        n = dcp_decode_window_workspace_size(desc, batch, q_len, window, n_sinks, rank=rank)
     if n == 0:
-        raise ValueError("unsupported cache descriptor for dcp_decode_rank")
+        raise ValueError("unsupported cache descriptor, query length or window for a rank's decode")
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
@@ -51,14 +58,19 @@ def exchange(o: torch.Tensor, lse: torch.Tensor, rank: int, world: int, group=No
 
 
 def decode_distributed(desc: CacheDesc, rank: int, world: int, q: torch.Tensor, seq_lens: torch.Tensor,
-                       ws: torch.Tensor, group=None):
+                       ws: torch.Tensor, group=None, window: int | None = None, n_sinks: int = 0):
     """One decode step of rank `rank` of a DCP group (desc: this rank's cache, block
     tables [1][B][max_local_pages]): its local partial, then the exchange.
-    q bf16 [B][hq][dk] or [B][q_len][hq][dk].  Returns (out, lse) as exchange(), with
+    q bf16 [B][hq][dk] or [B][q_len][hq][dk].  window: attend only that many positions and
+    the first n_sinks (dcp_decode_window).  Returns (out, lse) as exchange(), with
     rows = q_len * hq (row j * hq + h is query token j of head h)."""
     B = q.shape[0]
     rows = q.shape[-2] * (1 if q.dim() == 3 else q.shape[1])
     o = torch.empty((B, rows, desc.dv), dtype=torch.float32, device=q.device)
     lse = torch.empty((B, rows), dtype=torch.float32, device=q.device)
-    dcp_decode_rank(desc, rank, q, seq_lens, o.view(*q.shape[:-1], desc.dv), lse.view(q.shape[:-1]), ws)
+    o_q, lse_q = o.view(*q.shape[:-1], desc.dv), lse.view(q.shape[:-1])
+    if window is None:
+        dcp_decode_rank(desc, rank, q, seq_lens, o_q, lse_q, ws)
+    else:
+        dcp_decode_window(desc, q, seq_lens, window, n_sinks, o_q, lse_q, ws, rank=rank)
     return exchange(o, lse, rank, world, group)

@@ -16,8 +16,8 @@ import torch
 import synth
 import synth.device as sdev
 
-from . import (DCP_BF16, DCP_DECODE_RANK, DCP_FP8_E4M3, DCP_GQA, DCP_MLA, CacheDesc, dcp_decode_workspace_size,
-               dcp_decode_workspace_size_ex, dcp_kv_append, dcp_kv_append_rank, dcp_shard_counts, make_cache_desc)
+from . import (DCP_BF16, DCP_DECODE_RANK, DCP_FP4_E2M1, DCP_FP8_E4M3, DCP_GQA, DCP_MLA, CacheDesc,
+               dcp_decode_workspace_size, dcp_decode_workspace_size_ex, dcp_kv_append, dcp_kv_append_rank, dcp_shard_counts, make_cache_desc)
 
 
 @dataclass
@@ -66,8 +66,12 @@ def build(w: synth.Workload, counts_with_growth: np.ndarray, fill: bool = True, 
     bt_np, num_pages = synth.deal_block_tables(w.seed_len, need, slack_pages=slack_pages)
     bt = torch.as_tensor(bt_np, device=dev)
     kind = DCP_GQA if w.kind == "gqa" else DCP_MLA
-    dtype = DCP_FP8_E4M3 if w.dtype == "fp8" else DCP_BF16
-    if kind == DCP_GQA:
+    dtype = {"bf16": DCP_BF16, "fp8": DCP_FP8_E4M3, "fp4": DCP_FP4_E2M1}[w.dtype]
+    if dtype == DCP_FP4_E2M1:
+        k_pages = torch.empty((num_pages, w.hkv, P * (w.dk // 2 + w.dk // 16)), dtype=torch.uint8, device=dev)
+        v_pages = torch.empty_like(k_pages)
+        kv_scales = None
+    elif kind == DCP_GQA:
         k_pages = torch.empty((num_pages, w.hkv, P, w.dk), dtype=torch.bfloat16, device=dev)
         v_pages = torch.empty((num_pages, w.hkv, P, w.dv), dtype=torch.bfloat16, device=dev)
         kv_scales = None

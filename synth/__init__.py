@@ -234,7 +234,7 @@ def deal_block_tables(seed: int, pages_needed: np.ndarray, slack_pages: int = 0)
 class Workload:
     name: str
     kind: str            # "gqa" or "mla"
-    dtype: str           # "bf16" or "fp8"
+    dtype: str           # "bf16", "fp8" (mla) or "fp4" (gqa)
     B: int
     hq: int
     hkv: int
@@ -250,6 +250,8 @@ class Workload:
 
     @property
     def kv_bytes_per_token(self) -> int:
+        if self.dtype == "fp4":
+            return 2 * self.hkv * (self.dk // 2 + self.dk // 16)
         if self.kind == "gqa":
             return 2 * self.hkv * self.dk * 2
         return 576 * 2 if self.dtype == "bf16" else 576 + 4
