@@ -69,7 +69,8 @@ struct Lane {
     // what bounds it and two groups share the step's votes and hide each other's
     // latencies; bf16: one, since the bytes in flight are what counts.
     static constexpr int kStep = FP4 ? 2 : 1;
-    static constexpr int kSteps = FP4 ? (D == 128 ? 5 : 8) : (D == 128 ? 3 : 6);  // steps in the queue
+    // (4-bit: 5 steps of 128 dimensions measured 303 us against 300 for 3, 24 requests of 32k-128k tokens)
+    static constexpr int kSteps = FP4 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);  // steps in the queue
     static constexpr int kStages = kStep * kSteps;
 };
 
@@ -1047,59 +1048,67 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             mbar_wait(&s_full[warp][k % C::kSteps], (k / C::kSteps) & 1, nullptr, a.status);
 }
 
-// Sum of a segment's parts: worker w's tail and the heads of the workers after it up
-// to tail[w].z.  CTA (w, block of rows); `wpr` warps share a row's parts.
+// Sums of the segments that are in parts: the tail of worker w and the heads of the
+// workers after it up to tail[w].z.  CTA (x, block of rows): workers x, x + gridDim.x, ..,
+// 32 at most; `wpr` warps share a row's parts.
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ StreamArgs a, int D, int wpr) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete and visible
-    const int4 t = a.tail[blockIdx.x];
-    if (t.x < 0) return;
     __shared__ float s_w[8];
     __shared__ float4 s_o[8][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rpc = 8 / wpr;
     const int r = blockIdx.y * rpc + warp / wpr, part = warp % wpr;
-    const int g = t.y / a.tiles, tile = t.y - g * a.tiles;
-    const bool live = r < min(kRows, a.rows - tile * kRows);
-    const int K = t.z - (int)blockIdx.x + 1;  // parts
     const int nv = D / 4;
-    // part k's slot: the tail of the first worker, the heads of the others
-    auto slot = [&](int k) { return (int64_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)) * kRows + r; };
-    float M = -INFINITY, ws = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (live) {
-        for (int k = lane; k < K; k += 32) M = fmaxf(M, __ldg(a.part_lse + slot(k)));
+    const int mine = blockIdx.x + lane * gridDim.x;
+    uint32_t todo = __ballot_sync(0xffffffffu, mine < a.workers && a.tail[mine].x >= 0);  // the same in every warp
+    for (; todo; todo &= todo - 1) {
+        const int first = blockIdx.x + (__ffs(todo) - 1) * gridDim.x;
+        const int4 t = a.tail[first];
+        const int g = t.y / a.tiles, tile = t.y - g * a.tiles;
+        const bool live = r < min(kRows, a.rows - tile * kRows);
+        const int K = t.z - first + 1;  // parts
+        // part k's slot: the tail of the first worker, the heads of the others
+        auto slot = [&](int k) { return (int64_t)(2 * (first + k) + (k == 0 ? 1 : 0)) * kRows + r; };
+        float M = -INFINITY, ws = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live) {
+            for (int k = lane; k < K; k += 32) M = fmaxf(M, __ldg(a.part_lse + slot(k)));
 #pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        const float ref = M == -INFINITY ? 0.f : M;
+            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-        for (int k = part; k < K; k += wpr) {
-            const float e = __ldg(a.part_lse + slot(k));
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (lane < nv) x = __ldg(reinterpret_cast<const float4*>(a.part_o + slot(k) * D) + lane);
-            const float w = e == -INFINITY ? 0.f : exp2f(e - ref);
-            ws += w;
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
+            for (int k = part; k < K; k += wpr) {
+                const float e = __ldg(a.part_lse + slot(k));
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (lane < nv) x = __ldg(reinterpret_cast<const float4*>(a.part_o + slot(k) * D) + lane);
+                const float w = e == -INFINITY ? 0.f : exp2f(e - ref);
+                ws += w;
+                acc.x = fmaf(w, x.x, acc.x);
+                acc.y = fmaf(w, x.y, acc.y);
+                acc.z = fmaf(w, x.z, acc.z);
+                acc.w = fmaf(w, x.w, acc.w);
+            }
         }
+        s_w[warp] = ws;
+        s_o[warp][lane] = acc;
+        __syncthreads();
+        if (live && part == 0) {
+            for (int w = 1; w < wpr; w++) {
+                const float4 x = s_o[warp + w][lane];
+                ws += s_w[warp + w];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+            const float inv = ws == 0.f ? 0.f : 1.f / ws;
+            const Row row = out_row(a, t.x, g, tile, r, D);
+            if (lane < nv)
+                reinterpret_cast<float4*>(row.o)[lane] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (lane == 0) *row.lse = ws == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(ws)) * kLn2;
+        }
+        __syncthreads();
     }
-    s_w[warp] = ws;
-    s_o[warp][lane] = acc;
-    __syncthreads();
-    if (!live || part != 0) return;
-    for (int w = 1; w < wpr; w++) {
-        const float4 x = s_o[warp + w][lane];
-        ws += s_w[warp + w];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
-    }
-    const float inv = ws == 0.f ? 0.f : 1.f / ws;
-    const Row row = out_row(a, t.x, g, tile, r, D);
-    if (lane < nv) reinterpret_cast<float4*>(row.o)[lane] = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-    if (lane == 0) *row.lse = ws == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) + log2f(ws)) * kLn2;
 }
 
 __global__ void finish_init_kernel(int64_t* finish_ns, int64_t* t_start, int B) {
@@ -1123,10 +1132,19 @@ bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
     return (dk == 64 || dk == 128) && hq % hkv == 0 && q_len >= 1;
 }
 
-// Whole segments or equal shares.  The rule compares, in units of one group's work by a
-// warp, whole segments -- rounds times the longest segment the tables and the mask
-// allow -- with equal shares: the mean share, plus the scan of the lengths, the partials
-// and a second kernel.
+// Whole segments or equal shares.  The rule compares estimates in units of one group's
+// work by a warp (about 1 us): whole segments -- rounds times the longest segment that
+// the tables and the mask allow, plus what a segment costs beside its groups, more in a
+// team (its sum) and most where other teams share the SM -- and equal shares: the mean,
+// plus the scan of the lengths, the partials and a second kernel.  Measured: a window of
+// 128 (2 segments of about 11 groups) 8.0 us in a team of 4, 15.3 us a warp, 10.5 us in
+// shares; a window of 1021 (512 of 68) 57 us a warp, 65 us in teams, 71 us in shares; a
+// window of 4096 (512 of 258) 186 us in shares, 196 us in teams, 280 us a warp.
+// Shares: a team of 4 needs a fourth of the parts, a lone warp wastes nothing on short
+// segments: 48 requests of 1-14k tokens, 384 segments 47.3 us in teams, 49.6 us alone;
+// one request of 65536 tokens, 4 segments, 41 and 59 us.  lead: the same 48 requests 153,
+// 65, 49 and 47 us at 4, 16, 32 and 48 groups a segment (teams), 72, 53, 50 and 52 us at
+// 4, 8, 16 and 32 (a warp).
 StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
                            int num_sms) {
     StreamPlan p;
@@ -1141,9 +1159,10 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
     }
     const int64_t groups = (tokens / shards + kTok - 1) / kTok * span + 2 * span;
     const int64_t ctas = (int64_t)num_sms * kCtasPerSm, warps = ctas * kWarps;
-    const int64_t one = (segs + warps - 1) / warps * groups;
-    const int64_t four = (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + 6);
-    const int64_t share = (segs * (groups + 4) + warps - 1) / warps + 20;
+    const int64_t one = (segs + warps - 1) / warps * groups * (2 * segs <= warps ? 3 : 4) / 4 + 6;
+    const int64_t four =
+        (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + (2 * kWarps * segs > warps ? 14 : 8));
+    const int64_t share = (segs * (groups + 16) + warps - 1) / warps + 30;
     p.team = 1;
     p.whole = 1;
     int64_t best = one;
@@ -1155,7 +1174,7 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         p.whole = 0;
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
-    p.lead = p.team == 1 ? 8 : 32;
+    p.lead = p.team == 1 ? 16 : 48;
     const int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
     p.ctas = (int)(grid < ctas ? grid : ctas);
     p.workers = p.ctas * (kWarps / p.team);
@@ -1260,8 +1279,11 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     // few parts a segment: a row for each warp; many: a CTA for each row
     const int wpr = p.workers >= 8 * p.segs ? 8 : 1;
     const int rows = a.rows < kRows ? a.rows : kRows;
+    // at most one sum a segment: few segments take few CTAs (65536 tokens of 4 segments: 0.7 us less than a CTA for
+    // each of 296 workers); four for each segment, so that a CTA seldom has two sums; a CTA takes 32 workers at most
+    const int64_t least = (p.workers + 31) / 32, some = 4 * p.segs < p.workers ? 4 * p.segs : p.workers;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.workers, (unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
+    cfg.gridDim = dim3((unsigned)(some > least ? some : least), (unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr;  // the launch overlaps the kernel before it; combine_kernel waits for its end

@@ -34,7 +34,8 @@ struct StreamArgs {
     float* part_o;    // [2 * workers][kRows][D]
     float* part_lse;  // [2 * workers][kRows], log2
     float4* acc;      // [warps][kAcc] each warp's O between two flushes, or null
-    int4* tail;       // [workers]: segment that starts in the worker's share and ends in another's
+    int4* tail;  // [workers]: segment that starts in the worker's share and ends in another's: base, segment of
+                 // the base, last worker
     int* status;
     int64_t* finish_ns;
     const int64_t* t_start;
