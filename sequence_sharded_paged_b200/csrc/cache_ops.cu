@@ -153,6 +153,8 @@ __global__ void append_mla_fp8_kernel(AppendArgs a) {
 // 2 (D/2 + D/16) out for each head; what bounds it is the arithmetic of the codes.
 constexpr int kHeadsPerLane = 2;
 
+// A warp holds the same head's rows of four tokens that follow one another in the call:
+// in a prompt they do in a page too, and their scales are one word.
 struct RowLane {
     int64_t i;  // token
     int g0;     // first head
@@ -160,48 +162,68 @@ struct RowLane {
     int pg, off;
 };
 
+__device__ __forceinline__ int row_shift(const AppendArgs& a) { return a.dk == 128 ? 3 : 2; }  // log2 of D/16
+
 __device__ __forceinline__ RowLane row_lane(const AppendArgs& a) {
-    const int lpr = a.dk / 16;
+    const int shift = row_shift(a);
     const int hb = (a.hkv + kHeadsPerLane - 1) / kHeadsPerLane;
-    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
-    RowLane r{w / hb, 0, (int)(threadIdx.x % lpr), -2, 0};
-    r.g0 = (int)(w - r.i * hb) * kHeadsPerLane;
+    const int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> shift, four = w >> 2;
+    const int64_t t = four >> 32 ? four / hb : (int64_t)((uint32_t)four / (uint32_t)hb);
+    RowLane r{4 * t + (w & 3), (int)(four - t * hb) * kHeadsPerLane, (int)threadIdx.x & ((1 << shift) - 1), -2, 0};
     if (r.i < a.n_tok) r.pg = append_target(a, r.i, &r.off);
     if (r.pg == -1 && r.li == 0 && r.g0 == 0) record_status(a.status, DCP_ERR_UNALLOCATED_PAGE);
     return r;
 }
+static int64_t row_lanes(const AppendArgs& a) {
+    return (a.n_tok + 3) / 4 * 4 * ((a.hkv + kHeadsPerLane - 1) / kHeadsPerLane) * (a.dk / 16);
+}
 
-__device__ __forceinline__ void store_fp4x16(uint8_t* blk, int P, int D, int off, int li, const uint4* v,
-                                             float factor) {
+// Stores a lane's run: codes, and the scales of the warp's four tokens as a word where
+// they lie in one (`word`).  Executed by whole warps; `live`: this lane has a row.
+__device__ __forceinline__ void store_fp4x16(uint8_t* blk, int P, int D, int off, int li, const uint4* v, float factor,
+                                             bool live, bool word, int shift) {
     float s;
-    const uint8_t sb = fp4_scale(max2_nan(fp4_abs_max(v[0]), fp4_abs_max(v[1])), factor, &s);
+    const uint32_t sb = fp4_scale(max2_nan(fp4_abs_max(v[0]), fp4_abs_max(v[1])), factor, &s);
+    uint32_t all = sb | __shfl_down_sync(0xffffffffu, sb, 1 << shift) << 8;
+    all |= __shfl_down_sync(0xffffffffu, all, 2 << shift) << 16;
+    if (!live) return;
     *reinterpret_cast<uint2*>(blk + off * (D / 2) + li * 8) =
         make_uint2(fp4_codes8(v[0], s, factor), fp4_codes8(v[1], s, factor));
-    blk[P * (D / 2) + li * P + off] = sb;
+    uint8_t* scale = blk + P * (D / 2) + li * P + off;
+    if (!word)
+        *scale = (uint8_t)sb;
+    else if ((off & 3) == 0)
+        *reinterpret_cast<uint32_t*>(scale) = all;
 }
 
 __global__ void __launch_bounds__(256, 4) append_gqa_fp4_kernel(AppendArgs a) {
     const RowLane r = row_lane(a);
-    if (r.pg < 0) return;
-    const int P = a.page_size, D = a.dk;
+    const int P = a.page_size, D = a.dk, lane = threadIdx.x & 31, shift = row_shift(a);
+    // do the four tokens lie in one page, from a multiple of 4 on?
+    const int four = 3 << shift, first = lane & ~four;
+    const int pg0 = __shfl_sync(0xffffffffu, r.pg, first), off0 = __shfl_sync(0xffffffffu, r.off, first);
+    const bool fits = r.pg >= 0 && r.pg == pg0 && (off0 & 3) == 0 && r.off - off0 == (lane & four) >> shift;
+    const uint32_t tokens = (1u | 1u << (1 << shift) | 1u << (2 << shift) | 1u << (3 << shift)) << first;
+    const bool word = (__ballot_sync(0xffffffffu, fits) & tokens) == tokens;
     const float fk = a.kv_scales ? __ldg(a.kv_scales) : 1.f, fv = a.kv_scales ? __ldg(a.kv_scales + 1) : 1.f;
     uint4 k[kHeadsPerLane][2], v[kHeadsPerLane][2];
 #pragma unroll
     for (int e = 0; e < kHeadsPerLane; e++) {
-        if (r.g0 + e >= a.hkv) break;
+        const bool live = r.pg >= 0 && r.g0 + e < a.hkv;
         const int64_t at = ((r.i * a.hkv + r.g0 + e) * D + r.li * 16) * 2;
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            k[e][h] = __ldg(reinterpret_cast<const uint4*>(a.k_new + at) + h);
-            v[e][h] = __ldg(reinterpret_cast<const uint4*>(a.v_new + at) + h);
+            k[e][h] = v[e][h] = make_uint4(0, 0, 0, 0);
+            if (live) k[e][h] = __ldg(reinterpret_cast<const uint4*>(a.k_new + at) + h);
+            if (live) v[e][h] = __ldg(reinterpret_cast<const uint4*>(a.v_new + at) + h);
         }
     }
 #pragma unroll
     for (int e = 0; e < kHeadsPerLane; e++) {
-        if (r.g0 + e >= a.hkv) break;
+        const bool live = r.pg >= 0 && r.g0 + e < a.hkv;
         const int64_t blk = ((int64_t)r.pg * a.hkv + r.g0 + e) * fp4_block_bytes(P, D);
-        store_fp4x16(a.k_pages + blk, P, D, r.off, r.li, k[e], fk);
-        store_fp4x16(a.v_pages + blk, P, D, r.off, r.li, v[e], fv);
+        store_fp4x16(a.k_pages + blk, P, D, r.off, r.li, k[e], fk, live, word, shift);
+        store_fp4x16(a.v_pages + blk, P, D, r.off, r.li, v[e], fv, live, word, shift);
     }
 }
 
@@ -316,8 +338,7 @@ cudaError_t launch_shard_map(int64_t n_pos, const int32_t* pos, const int32_t* r
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
     if (a.n_tok == 0) return cudaSuccess;
     if (a.dtype == DCP_FP4_E2M1) {
-        const int64_t groups = a.n_tok * ((a.hkv + kHeadsPerLane - 1) / kHeadsPerLane);
-        append_gqa_fp4_kernel<<<blocks_for(groups * (a.dk / 16), 256), 256, 0, s>>>(a);
+        append_gqa_fp4_kernel<<<blocks_for(row_lanes(a), 256), 256, 0, s>>>(a);
     } else if (a.kind == DCP_GQA) {
         append_gqa_kernel<<<blocks_for(a.n_tok * a.hkv * 32, 256), 256, 0, s>>>(a);
     } else if (a.dtype == DCP_BF16) {
@@ -331,9 +352,8 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
 cudaError_t launch_gather(const AppendArgs& a, void* k_out, void* v_out, cudaStream_t s) {
     if (a.n_tok == 0) return cudaSuccess;
     if (a.kind == DCP_GQA) {
-        const int64_t groups = a.n_tok * ((a.hkv + kHeadsPerLane - 1) / kHeadsPerLane);
         (a.dtype == DCP_FP4_E2M1 ? gather_gqa_kernel<true> : gather_gqa_kernel<false>)
-            <<<blocks_for(groups * (a.dk / 16), 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out),
+            <<<blocks_for(row_lanes(a), 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out),
                                                                    static_cast<uint8_t*>(v_out));
     } else {
         gather_mla_kernel<<<blocks_for(a.n_tok * 32, 256), 256, 0, s>>>(a, static_cast<uint8_t*>(k_out));

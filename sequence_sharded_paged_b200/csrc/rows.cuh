@@ -84,7 +84,6 @@ __device__ __forceinline__ uint32_t fp4_abs_max(const uint4& v) {
 // Codes of 8 bf16 values against a scale (zero or NaN: zero codes).  The scale is the
 // rounded one, so a value may lie past 6 and saturates there.
 __device__ __forceinline__ uint32_t fp4_codes8(const uint4& v, float s, float factor) {
-    uint32_t w = 0;
     if (s > 0.f) {
         float x[8];
         unpack8(v, x);
@@ -96,12 +95,18 @@ __device__ __forceinline__ uint32_t fp4_codes8(const uint4& v, float s, float fa
 #pragma unroll
             for (int e = 0; e < 8; e++) x[e] = __fdiv_rn(x[e], s);
         }
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e], x[2 * e + 1]), __NV_E2M1, cudaRoundNearest)
-                 << (8 * e);
+        uint32_t w;
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+            "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+            "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+            : "=r"(w)
+            : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+        return w;
     }
-    return w;
+    return 0;
 }
 
 // Quantise a run of 16 bf16 values held by two neighbouring lanes, 8 each: returns
