@@ -12,14 +12,19 @@
 // are within 2^-33 turns of it.
 //
 // Bound by HBM: every row is read once and written once, 4 D bytes, so what has to be
-// kept down are the instructions for each row.  A row is D/8 lanes of 8 dimensions.
-// With the HALF layout a rotated lane holds dimensions 4 i .. 4 i + 3 and their
-// partners rot_dim/2 further, so that neither layout exchanges anything between lanes;
-// the mean is a shuffle sum.  Cosine and sine are computed once for each token and
+// kept down are the instructions for each row.  A row is D/16 lanes that hold two
+// chunks of 8 dimensions each, half of the rotated (or of the other) dimensions apart:
+// neither layout then exchanges anything between lanes, and a warp's accesses are whole
+// lines.  The mean is a shuffle sum.  Cosine and sine are computed once for each token and
 // pair and shared by all heads through shared memory; a block takes up to 8 tokens, so
 // that positions, tables and angles are looked up side by side.  Rows of a 4-bit cache
-// need 16 consecutive dimensions in two neighbouring lanes instead (one scale), and
-// exchange the pairs by shuffles.
+// need 16 consecutive dimensions in two neighbouring lanes instead (one scale): D/8
+// lanes of 8 dimensions, which exchange the pairs by shuffles.
+//
+// Measured: 16384 tokens of 64 + 4 + 4 heads of 128, half rotated, 604 MB: 110 us, 5.5
+// TB/s, 84% of a copy's rate (8 dimensions a lane: 125 us; 16 and the loads of two rows
+// ahead, with half the blocks: 120-124 us).  4001 tokens of the MLA latent and 64
+// absorbed queries, 599 MB: 105 us, 5.7 TB/s.  128 tokens: 4.3 us, a launch's latency.
 //
 // Where rows are placed follows "Efficient Decode Context Parallelism with vLLM for
 // Long Context Workloads", section 4 (a position's row lies on its owner).
@@ -109,10 +114,14 @@ __device__ __forceinline__ Target find_target(const AppendArgs& a, int64_t i) {
 
 // FP4: the cache is a 4-bit one.
 template <int D, bool FP4>
-__global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_constant__ NormRopeArgs n,
-                                                                 const __grid_constant__ dcp_rope rope) {
-    constexpr int LPR = D / 8;             // lanes per row
+__global__ void __launch_bounds__(kThreads, 4) norm_rope_gqa_kernel(const __grid_constant__ NormRopeArgs n,
+                                                                    const __grid_constant__ dcp_rope rope) {
+    constexpr int V = FP4 ? 1 : 2;          // chunks of 8 dimensions a lane
+    constexpr int LPR = D / (8 * V);        // lanes per row
     constexpr int GROUPS = kThreads / LPR;  // rows in flight
+    struct Chunks {
+        uint4 v[V];
+    };
     __shared__ __align__(16) float2 s_cs[kMaxTokens * DCP_ROPE_MAX_PAIRS];
     __shared__ Target s_target[kMaxTokens];
     const AppendArgs& a = n.a;
@@ -124,11 +133,12 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_co
     const int nq = n.q ? n.hq : 0, nk = a.k_new ? a.hkv : 0;
     const int rows = nq + 2 * nk;  // queries, keys, values of one token
 
-    // this lane's dimensions: o0 .. o0 + 3 and o1 .. o1 + 3
-    const int rot_lanes = n.rotate ? rope.rot_dim / 8 : 0;
+    // this lane's dimensions: chunks at o0 and, apart by half of the rotated or of the
+    // other dimensions, at o1
+    const int rot_lanes = n.rotate ? rope.rot_dim / (8 * V) : 0;
     const bool turns = li < rot_lanes, half = rope.layout == DCP_ROPE_HALF;
-    const bool apart = !FP4 && turns && half;
-    const int o0 = apart ? 4 * li : 8 * li, o1 = apart ? rope.rot_dim / 2 + 4 * li : 8 * li + 4;
+    const int part = turns ? 8 * V * rot_lanes : D - 8 * V * rot_lanes;  // dimensions of the part
+    const int o0 = FP4 || turns ? 8 * li : 8 * (V - 1) * rot_lanes + 8 * li, o1 = o0 + part / 2;
 
     // rows are numbered token by token; a group steps GROUPS rows at a time
     struct At {
@@ -141,9 +151,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_co
             p.t++;
         }
     };
-    auto load = [&](const uint8_t* row) -> uint4 {  // not read-only loads: q_out may be q
-        const uint2 x = *reinterpret_cast<const uint2*>(row + o0 * 2), y = *reinterpret_cast<const uint2*>(row + o1 * 2);
-        return make_uint4(x.x, x.y, y.x, y.y);
+    auto load = [&](const uint8_t* row) -> Chunks {  // not read-only loads: q_out may be q
+        Chunks w;
+        w.v[0] = *reinterpret_cast<const uint4*>(row + o0 * 2);
+        if (V == 2) w.v[V - 1] = *reinterpret_cast<const uint4*>(row + o1 * 2);
+        return w;
     };
     auto source = [&](const At& p) -> const uint8_t* {
         const int64_t i = i0 + p.t;
@@ -162,19 +174,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_co
         }
         return base + (at + h * D) * 2;
     };
-    auto store = [&](uint8_t* row, const uint4& w) {
-        *reinterpret_cast<uint2*>(row + o0 * 2) = make_uint2(w.x, w.y);
-        *reinterpret_cast<uint2*>(row + o1 * 2) = make_uint2(w.z, w.w);
+    auto store = [&](uint8_t* row, const Chunks& w) {
+        *reinterpret_cast<uint4*>(row + o0 * 2) = w.v[0];
+        if (V == 2) *reinterpret_cast<uint4*>(row + o1 * 2) = w.v[V - 1];
     };
-    // the first rows' loads overlap the positions', tables' and angles' work
-    uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
-    At p0{0, grp - GROUPS}, p1;
+    // a group's next row is loaded beside the work on this one; the first rows' loads overlap the positions', tables' and angles' work
+    Chunks w0 = {};
+    At p0{0, grp - GROUPS};
     next(p0);
-    p1 = p0;
-    next(p1);
     if (p0.t < nt) w0 = load(source(p0));
-    if (p1.t < nt) w1 = load(source(p1));
-    uint4 qw = make_uint4(0, 0, 0, 0), kw = qw;
+    Chunks qw = {}, kw = {};
     if (n.q_weight) qw = load(n.q_weight);
     if (n.k_weight) kw = load(n.k_weight);
 
@@ -193,45 +202,58 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_co
     const float fk = FP4 && a.kv_scales && nk ? __ldg(a.kv_scales) : 1.f;
     const float fv = FP4 && a.kv_scales && nk ? __ldg(a.kv_scales + 1) : 1.f;
 
-    auto process = [&](const At& p, uint4 w) {
+    auto process = [&](const At& p, Chunks w) {
         const int t = p.t, h = p.h;
         const Target tg = s_target[t];
         const bool is_q = h < nq;
         if (h < nq + nk) {
             const bool weight = is_q ? n.q_weight != nullptr : n.k_weight != nullptr;
             if (weight || rot_lanes) {  // otherwise the row goes through bit for bit
-                float x[8];
-                unpack8(w, x);
+                float x[V][8];
+#pragma unroll
+                for (int c = 0; c < V; c++) unpack8(w.v[c], x[c]);
                 if (weight) {
                     float ss = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+                    for (int c = 0; c < V; c++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) ss = fmaf(x[c][e], x[c][e], ss);
 #pragma unroll
                     for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
                     const float inv = rsqrtf(fmaf(ss, 1.f / D, n.eps));
-                    float wt[8];
-                    unpack8(is_q ? qw : kw, wt);
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = x[e] * inv * wt[e];
+                    for (int c = 0; c < V; c++) {
+                        float wt[8];
+                        unpack8(is_q ? qw.v[c] : kw.v[c], wt);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[c][e] = x[c][e] * inv * wt[e];
+                    }
                 }
                 const float2* cs = s_cs + t * DCP_ROPE_MAX_PAIRS;
                 if (FP4) {
-                    rotate8(x, cs, rope.layout, rot_lanes / 2, li, base_lane, mask);
-                } else if (turns) {
-                    const float4* c4 = reinterpret_cast<const float4*>(cs + 4 * li);
+                    rotate8(x[0], cs, rope.layout, rot_lanes / 2, li, base_lane, mask);
+                } else if (turns && half) {
+                    const float4* c4 = reinterpret_cast<const float4*>(cs + o0);  // pairs o0 .. o0 + 7
 #pragma unroll
-                    for (int e = 0; e < 2; e++) {
-                        const float4 c = c4[e];  // pairs 2e and 2e + 1: cos, sin, cos, sin
-                        if (half) {
-                            turn(x[2 * e], x[2 * e + 4], c.x, c.y);
-                            turn(x[2 * e + 1], x[2 * e + 5], c.z, c.w);
-                        } else {
-                            turn(x[4 * e], x[4 * e + 1], c.x, c.y);
-                            turn(x[4 * e + 2], x[4 * e + 3], c.z, c.w);
+                    for (int e = 0; e < 4; e++) {
+                        const float4 c = c4[e];  // cos, sin, cos, sin
+                        turn(x[0][2 * e], x[V - 1][2 * e], c.x, c.y);
+                        turn(x[0][2 * e + 1], x[V - 1][2 * e + 1], c.z, c.w);
+                    }
+                } else if (turns) {
+#pragma unroll
+                    for (int k = 0; k < V; k++) {
+                        const float4* c4 = reinterpret_cast<const float4*>(cs + (k ? o1 : o0) / 2);
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const float4 c = c4[e];
+                            turn(x[k][4 * e], x[k][4 * e + 1], c.x, c.y);
+                            turn(x[k][4 * e + 2], x[k][4 * e + 3], c.z, c.w);
                         }
                     }
                 }
-                w = pack8(x);
+#pragma unroll
+                for (int c = 0; c < V; c++) w.v[c] = pack8(x[c]);
             }
         }
         if (is_q) {
@@ -243,19 +265,16 @@ __global__ void __launch_bounds__(kThreads) norm_rope_gqa_kernel(const __grid_co
         const int g = h - nq - (is_k ? 0 : nk);
         uint8_t* pool = is_k ? a.k_pages : a.v_pages;
         if (FP4)
-            store_gqa8(a, pool, tg.pg, g, tg.off, li, w, is_k ? fk : fv, mask, true);
+            store_gqa8(a, pool, tg.pg, g, tg.off, li, w.v[0], is_k ? fk : fv, mask, true);
         else
             store(pool + (((int64_t)tg.pg * a.hkv + g) * a.page_size + tg.off) * (D * 2), w);
     };
     while (p0.t < nt) {
-        const uint4 c0 = w0, c1 = w1;
-        const At a0 = p0, a1 = p1;
-        next(p0), next(p0);
-        next(p1), next(p1);
+        const Chunks c0 = w0;
+        const At a0 = p0;
+        next(p0);
         if (p0.t < nt) w0 = load(source(p0));
-        if (p1.t < nt) w1 = load(source(p1));
         process(a0, c0);
-        if (a1.t < nt) process(a1, c1);
     }
 }
 
