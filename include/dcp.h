@@ -264,7 +264,8 @@ dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double
  *             NULL: k's rows are not normed.
  *  eps        >= 0: y = x / sqrt(mean x^2 + eps) * weight.
  *  q_out      bf16 [n_tok][hq][dk], NULL only without q.  May be q itself when
- *             q_stride = hq * dk (MLA then touches the rotated part only).
+ *             q_stride = hq * dk (MLA then touches the rotated part only); apart
+ *             from everything else that the call reads.
  * Norm and rotation are computed in 32 bits and rounded to bf16 once; a quantised
  * cache then stores that row as dcp_kv_append would.  Strides are multiples of 8
  * elements.  Two tokens with the same (req, pos) race, as in dcp_kv_append.  Rows
@@ -502,6 +503,11 @@ dcp_status dcp_lse_rescale(int32_t N, int32_t rank, int32_t B, int32_t H, int32_
  *  workload) does not fit at any N on a 148-SM part: its query split alone
  *  takes 37.9 MB and the smallest split area 39 MB; such callers use
  *  dcp_decode_partial with a workspace.
+ *  A 4-bit cache has no plan of that kind and always fits: with W = 8 warps for
+ *  each SM its decode takes at most
+ *    W * (128 * (dk+1) + 16)     the two ends of each share and their LSE
+ *    W * 8704                    sums between two stores
+ *  bytes, each term rounded up to 256: 30 MB on a 148-SM part.
  *  The plan kernel, first on `stream`, clears the scratch's work ticket and
  *  done counters; nothing else in it needs initialising.
  *  Calls that can overlap in time (different streams, or threads without an

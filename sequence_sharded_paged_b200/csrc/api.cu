@@ -554,6 +554,14 @@ dcp_status dcp_norm_rope_append(const dcp_cache_desc* cache, int32_t rank, const
         const uintptr_t a = reinterpret_cast<uintptr_t>(q), z = a + 2 * ((n_tok - 1) * q_stride + q_row);
         const uintptr_t oa = reinterpret_cast<uintptr_t>(q_out), oz = oa + 2 * n_tok * q_row;
         if (oa < z && a < oz && !(oa == a && q_stride == q_row)) return DCP_ERR_INVALID_ARG;
+        // and apart from whatever else is read
+        auto overlaps = [&](const void* p, int64_t elements) {
+            const uintptr_t x = reinterpret_cast<uintptr_t>(p);
+            return p && oa < x + 2 * elements && x < oz;
+        };
+        if (overlaps(k, (n_tok - 1) * k_stride + k_row) || overlaps(v, (n_tok - 1) * v_stride + k_row) ||
+            overlaps(q_weight, cache->dk) || overlaps(k_weight, mla ? cache->dv : cache->dk))
+            return DCP_ERR_INVALID_ARG;
     }
     int* status = nullptr;
     int num_sms = 0;

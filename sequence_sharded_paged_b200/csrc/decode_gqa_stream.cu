@@ -18,29 +18,49 @@
 // a share may then be parts of a segment, whose (O, LSE) go to the workspace and are
 // summed by combine_kernel.
 //
-// Tile: 16 query rows x 16 tokens on mma.sync m16n8k16 with fp32 accumulators.  Only
-// one token is read for 16 query rows at most, so the tensor pipe is far from its
-// limit and what counts is that the bytes arrive in the layout in which the
-// instruction wants them.  The dimensions of a k-step and the tokens of a group may
-// be permuted freely (Q, and P from S, are permuted alike), so each thread takes 16
-// (4-bit: 16 or 8) CONSECUTIVE bytes of a row as its operands:
+// Tile: 16 query rows x 16 tokens on mma.sync m16n8k16 with fp32 accumulators.
+//
+// bf16 caches.  Bound by HBM.  A group of K and of V arrives by one TMA copy each
+// (box: 16 tokens of a head, 128-byte swizzle) in a queue of 3 groups (6 for 64
+// dimensions) of the warp's own, with an mbarrier for each place and no other wait;
+// ldmatrix hands out K's operands, ldmatrix.trans V's.  (Copies by each thread of its
+// own bytes stayed at 4.1 TB/s however deep the queue; a barrier for K and one for V,
+// with K a group ahead: 220 us instead of 195 us.)  Q K^T is exact products, P has
+// three bf16 terms (24 bits), and O is summed by additions that round.
+//
+// 4-bit caches.  Bound by the arithmetic: codes to fp16, times their scale, and 16 + 32
+// matrix instructions (16 + 16 up to 8 rows) a group, which take at least 192 us of
+// the 299 us below.  The dimensions of a k-step and the tokens of a group may be
+// permuted freely (Q, and P from S, are permuted alike), so each thread takes 16 or 8
+// CONSECUTIVE bytes of a row as its operands:
 //   Q K^T  thread (n = lane / 4, c = lane % 4), token tile t: token
-//          4 (n >> 1) + 2 t + (n & 1); dimensions 32 c .. (4-bit) or
-//          32 i + 8 c .. + 7 (bf16, i-th 16 bytes);
+//          4 (n >> 1) + 2 t + (n & 1), dimensions D/4 c .. + D/4 - 1;
 //   P V    thread (n, c): tokens 4 c .. 4 c + 3, dimensions n D/8 .. + D/8 - 1 (n-tile
 //          j is dimension n D/8 + j); S leaves tokens 4 c .. 4 c + 3 in thread c.
 // So no data is exchanged between threads: every thread copies (cp.async) exactly the
-// bytes it will use into its own slots of a shared-memory queue, several groups ahead,
-// and the only wait in the kernel is the thread's own cp.async.wait_group.  Tokens
-// that no row may see are filled with zeros by the copy itself, so that stale or
-// non-finite bytes in masked places never meet a product.
+// bytes it will use into its own places of the queue, and waits for its own copies
+// only.  Tokens that no row may see are filled with zeros by the copy itself, so that
+// stale or non-finite bytes in masked places never meet a product.  Code times scale
+// has 6 significant bits and lies within 2^-10 .. 2688, so it is exact in fp16; q is
+// scaled by a power of two into fp16's range; P has two fp16 terms, with the reference
+// 2^7 below the maximum so that small weights stay above fp16's smallest step.
 //
-// Precision: bf16 caches: Q K^T in bf16 (exact products), P in two bf16 terms (16
-// bits).  4-bit caches: code times scale has 6 significant bits and lies within
-// 2^-10 .. 2688, so it is exact in fp16; q is scaled by a power of two into fp16's
-// range; P in two fp16 terms, with the reference 2^7 below the maximum so that small
-// weights stay above fp16's smallest step.  With at most 8 query rows the two terms
-// share one instruction (rows 0..7 and 8..15 of the tile); with more they take two.
+// With at most 8 query rows two terms of P share one instruction (rows 0..7 and 8..15
+// of the tile).  The scores of the next groups are computed beside P V of these, two
+// independent streams of instructions; what hides latency is that and a second block
+// on the SM, both out of registers (three blocks of 168 registers spill and are no
+// faster with 8 rows, slower with 16).
+//
+// Measured, K and V bytes / time, of a copy's 6.56 TB/s:
+//   bf16   128 requests, 64 / 4 heads of 128, window 4096: 1081 MB, 186 us, 5.8 TB/s, 89%
+//          1 request, window 65536: 134 MB, 41 us (20 us of it streaming, 9 us until the
+//          first bytes, the rest the sums of 300 parts and two launches)
+//          1 request, window 128, 8 / 2 heads of 64: 8 us, latency
+//   4-bit  24 requests of 32k-128k, 64 / 4 heads: 906 MB, 299 us, 3.0 TB/s (the instructions)
+//          48 requests of 1-14k, 64 / 8 heads: 85 MB, 47 us (8 rows; half of the segments
+//          are of 5 groups and cost as much as 48)
+//          64 requests, 4 tokens each, window 1021: 68 MB, 57 us (512 segments, a warp each)
+//          2 requests of 400, 8 / 2 heads of 64: 8 us, latency
 #include "common.cuh"
 #include "finish.cuh"
 #include "kernels.h"

@@ -101,6 +101,26 @@ def test_norm_rope_refusals():
     assert call(**{**m, "rope": r64, "v": A}) == INVALID and call(**{**m, "rope": r64, "qw": A}) == INVALID
 
 
+@pytest.mark.parametrize("which", ["q", "k", "v", "qw", "kw"])
+def test_norm_rope_refuses_an_output_that_overlaps_an_input(which):
+    L = dcp.lib()
+    rope = dcp.make_rope(128)
+    far = dict(q=1 << 30, k=2 << 30, v=3 << 30, qw=4 << 30, kw=5 << 30)
+    size = dict(q=2 * 2 * 16 * 128, k=2 * (1024 + 512), v=2 * (1024 + 512), qw=256, kw=256)[which]  # bytes read
+
+    def call(out):
+        p = far
+        return L.dcp_norm_rope_append(ctypes.byref(gqa()), 0, ctypes.byref(rope), 2, A, A, p["q"], 2048, p["k"], 1024,
+                                      p["v"], 1024, p["qw"], p["kw"], 1e-6, out, None)
+
+    out_bytes = 2 * 2 * 16 * 128
+    assert call(far[which] + size - 16) == INVALID
+    assert call(far[which] - out_bytes + 16) == INVALID
+    # next to it: passes the checks (and fails for want of a GPU, or is not reached on one)
+    if not torch.cuda.is_available():
+        assert call(far[which] + size) == dcp.DCP_ERR_CUDA and call(far[which] - out_bytes) == dcp.DCP_ERR_CUDA
+
+
 def test_rope_refusals():
     L, r = dcp.lib(), dcp.Rope()
     call = lambda rot=64, layout=0, theta=1e4, kind=0, factor=1.0, original=0.0, low=0.0, high=0.0, attn=0.0: L.dcp_rope_init(  # noqa: E731
