@@ -165,3 +165,85 @@ def test_4bit_shares_of_many_groups(group):
     tol_o = (2 * 1400 * 2.0 ** -23 + 2 * 2.1e-5) * float(v.abs().max())
     assert (out.double().cpu() - O).abs().max() <= tol_o
     assert (lse.double().cpu() - lse_ref).abs().max() <= 5e-5 + 700 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("start,T", [(0, 4), (0, 130), (1, 7), (2, 3), (3, 61), (5, 200), (64, 1)])
+@pytest.mark.parametrize("d,hkv,page,n,i", [(64, 3, 16, 2, 16), (128, 1, 64, 1, 1), (128, 2, 16, 3, 5)])
+def test_4bit_append_of_consecutive_tokens(d, hkv, page, n, i, start, T):
+    """Prompt rows from any first position: stored exactly, nothing beside them touched, and read back into
+    tensors that begin on a 16-byte boundary only."""
+    pages = 24
+    rng = np.random.default_rng(T + d)
+    bt = torch.as_tensor(rng.permutation(n * pages).astype(np.int32).reshape(n, 1, pages)).cuda()
+    block = page * (d // 2 + d // 16)
+    kp, vp = (torch.full((n * pages, hkv, block), 0xA5, dtype=torch.uint8, device="cuda") for _ in range(2))
+    desc = dcp.make_cache_desc(kind=dcp.DCP_GQA, dtype=dcp.DCP_FP4_E2M1, n_shards=n, interleave=i, page_size=page,
+                               num_pages=n * pages, hq=hkv, hkv=hkv, dk=d, dv=d, scale=1.0, batch=1, block_tables=bt,
+                               k_pages=kp, v_pages=vp)
+    pos = np.arange(start, start + T)
+    k, v = (bf16(rng.standard_normal((T, hkv, d)) * 5) for _ in range(2))
+
+    def at16(x):  # a copy of x that lies 16 bytes after a 32-byte boundary
+        room = torch.empty(x.numel() + 8, dtype=torch.bfloat16, device="cuda")
+        room[8:] = x.flatten()
+        return room[8:].view(x.shape)
+
+    dpos = torch.as_tensor(pos.astype(np.int32)).cuda()
+    req = torch.zeros_like(dpos)
+    dcp.dcp_kv_append(desc, req, dpos, at16(to_bf16(k)), at16(to_bf16(v)))
+    for pool, x in ((kp, k), (vp, v)):
+        code, sb, _ = quantise4(x)
+        want = np.full((n * pages, hkv, block), 0xA5, np.uint8)
+        for t, p in enumerate(pos):
+            loc = (p // (i * n)) * i + p % i
+            pg, off = int(bt[(p // i) % n, 0, loc // page]), loc % page
+            want[pg, :, off * (d // 2):(off + 1) * (d // 2)] = code[t][:, 0::2] | (code[t][:, 1::2] << 4)
+            want[pg, :, page * (d // 2) + np.arange(d // 16) * page + off] = sb[t].T
+        np.testing.assert_array_equal(pool.cpu().numpy(), want)
+    for shift in (0, 8):
+        ko, vo = (torch.empty(T * hkv * d + 8, dtype=torch.bfloat16, device="cuda")[shift:shift + T * hkv * d]
+                  .view(T, hkv, d) for _ in range(2))
+        dcp.dcp_kv_gather(desc, req, dpos, ko, vo)
+        np.testing.assert_array_equal(ko.double().cpu().numpy(), quantise4(k)[2])
+        np.testing.assert_array_equal(vo.double().cpu().numpy(), quantise4(v)[2])
+
+
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_4bit_decode_on_two_streams_and_in_a_graph(q_len):
+    """Two calls at once with a workspace each, and a captured call replayed after the cache has grown."""
+    hq, hkv, d = 16, 2, 128
+    rng = np.random.default_rng(77)
+    c = Cache("fp4", [rows(rng, L, hkv, d) for L in (700, 9, 3000)], [rows(rng, L, hkv, d) for L in (700, 9, 3000)],
+              hq=hq, hkv=hkv, d=d, page=16, n=2, i=16, room=40)
+    size = dcp.dcp_decode_workspace_size_ex(c.desc, 3, q_len, dcp.DCP_DECODE_MERGED)
+    shape = (3, q_len, hq, d)
+    q = [bf16(rng.standard_normal(shape)) for _ in range(2)]
+    dq = [to_bf16(x) for x in q]
+    out = [torch.empty(shape, device="cuda") for _ in range(2)]
+    lse = [torch.empty(shape[:3], device="cuda") for _ in range(2)]
+    ws = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            dcp.dcp_decode_merged(c.desc, dq[k], c.seq_lens, out[k], lse[k], ws[k], stream=s)
+    torch.cuda.synchronize()
+    vmax = max(np.abs(x).max() for x in c.v)
+    for k in range(2):
+        check(f"stream {k}", out[k], lse[k], *attention(c, q[k]), vmax)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dcp.dcp_decode_merged(c.desc, dq[0], c.seq_lens, out[0], lse[0], ws[0])
+        dcp.dcp_decode_merged(c.desc, dq[1], c.seq_lens, out[1], lse[1], ws[0])  # in order: the same workspace
+    new_k, new_v = rows(rng, 3, hkv, d), rows(rng, 3, hkv, d)
+    dcp.dcp_kv_append(c.desc, None, c.seq_lens, to_bf16(new_k), to_bf16(new_v))
+    c.seq_lens += 1
+    for b in range(3):
+        c.k[b] = np.concatenate((c.k[b], quantise4(new_k[b:b + 1])[2]))
+        c.v[b] = np.concatenate((c.v[b], quantise4(new_v[b:b + 1])[2]))
+    c.lengths = c.lengths + 1
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for k in range(2):
+        check(f"replay {k}", out[k], lse[k], *attention(c, q[k]), vmax)
