@@ -12,7 +12,7 @@
 //
 // Work: a segment is (request, KV head, tile of 16 query rows) -- of one shard when
 // partials are asked for, of all shards otherwise.  Its visible local positions are
-// read in groups of 16 tokens; a group never leaves its page.  A team of 1 or 4
+// read in groups of 16 tokens; a group never leaves its page.  A team of 1, 2 or 4
 // warps takes whole segments (short windows: one launch, nothing to merge), or an
 // equal share of the flat list of all groups, whatever the lengths; the two ends of
 // a share may then be parts of a segment, whose (O, LSE) go to the workspace and are
@@ -52,14 +52,14 @@
 // faster with 8 rows, slower with 16).
 //
 // Measured, K and V bytes / time, of a copy's 6.56 TB/s:
-//   bf16   128 requests, 64 / 4 heads of 128, window 4096: 1081 MB, 186 us, 5.8 TB/s, 89%
+//   bf16   128 requests, 64 / 4 heads of 128, window 4096: 1081 MB, 184 us, 5.9 TB/s, 90%
 //          1 request, window 65536: 134 MB, 41 us (20 us of it streaming, 9 us until the
 //          first bytes, the rest the sums of 300 parts and two launches)
 //          1 request, window 128, 8 / 2 heads of 64: 8 us, latency
 //   4-bit  24 requests of 32k-128k, 64 / 4 heads: 906 MB, 299 us, 3.0 TB/s (the instructions)
 //          48 requests of 1-14k, 64 / 8 heads: 85 MB, 47 us (8 rows; half of the segments
 //          are of 5 groups and cost as much as 48)
-//          64 requests, 4 tokens each, window 1021: 68 MB, 57 us (512 segments, a warp each)
+//          64 requests, 4 tokens each, window 1021: 68 MB, 48.5 us (512 segments, two warps each)
 //          2 requests of 400, 8 / 2 heads of 64: 8 us, latency
 #include "common.cuh"
 #include "finish.cuh"
@@ -71,8 +71,7 @@ namespace dcp {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 2;  // by registers and by the queues' sizes
-constexpr int kThreads = 32 * kWarps;
+constexpr int kWarpsPerSm = 8;  // by registers and by the queues' sizes
 constexpr int kAcc = 17 * 32;  // float4 of a warp's O in memory, and what belongs to it
 constexpr int kDescs = 64;   // group descriptors per warp (two batches of 32)
 
@@ -754,8 +753,9 @@ struct Warp {
 
 // Two CTAs of four warps for each SM: what hides latency here is independent work
 // within a warp, which takes registers, more than a third CTA would.
-template <bool FP4, int D, bool HALF>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
+// WARPS: 4, in teams of 1 or 4, or 2, a team that takes whole segments.
+template <bool FP4, int D, bool HALF, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, kWarpsPerSm / WARPS) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
     using W = Warp<FP4, D, HALF>;
     using C = Lane<FP4, D>;
     constexpr int S = C::kStages;
@@ -767,15 +767,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     // the swizzle of the bf16 stages goes by the address: 1024-byte alignment
     uint8_t* smem = FP4 ? smem_raw
                         : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t s_full[kWarps][C::kSteps];  // bf16: a stage's copies have landed
+    __shared__ uint64_t s_full[WARPS][C::kSteps];  // bf16: a stage's copies have landed
     __shared__ volatile int s_abort;
-    __shared__ Desc s_desc[kWarps][kDescs];
-    __shared__ float s_m[kWarps][16], s_l[kWarps][16], s_ol[kWarps][16];
-    __shared__ ShareScratch<kWarps> s_share;
+    __shared__ Desc s_desc[WARPS][kDescs];
+    __shared__ float s_m[WARPS][16], s_l[WARPS][16], s_ol[WARPS][16];
+    __shared__ ShareScratch<WARPS> s_share;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int team = warp / a.team, wt = warp - team * a.team;  // team of the CTA, warp of the team
-    const int teams = kWarps / a.team;
+    auto size = [&]() { return WARPS == 2 ? 2 : a.team; };  // warps of a team
+    auto whole = [&]() { return WARPS == 2 || a.whole; };
+    const int team = warp / size(), wt = warp - team * size();  // team of the CTA, warp of the team
+    const int teams = WARPS / size();
     const int worker = blockIdx.x * teams + team;
     uint8_t* ring = smem + (size_t)warp * kRing;
     const uint32_t ring_u32 = smem_u32(ring);
@@ -801,11 +803,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     // this worker's share: segments [worker, ..) step `workers`, or flat groups [r0, r1); no
     // share below 8 groups a warp, a partial costs about as much as those
     Share sh{0, 0, 0, 0, 0, 0, 0};
-    if (!a.whole) sh = find_share<kWarps>(a, nb, per_base, teams, team, 8ll * a.team, s_share);
+    if (!whole()) sh = find_share<WARPS>(a, nb, per_base, teams, team, 8ll * size(), s_share);
     int base = sh.base, sub = sh.sub, x0 = sh.x0;
     const typename W::Places places(a);
     // this lane's column of its warp's O in memory
-    auto acc = [&]() { return a.acc + ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kAcc + (threadIdx.x & 31); };
+    auto acc = [&]() { return a.acc + ((int64_t)blockIdx.x * WARPS + (threadIdx.x >> 5)) * kAcc + (threadIdx.x & 31); };
     uint32_t issued = 0, landed = 0;  // bf16: steps issued, and waited for
     uint32_t started = 0;             // lane 0: issued steps whose copies were started (all, but after a timeout)
     int4 tail = make_int4(-1, 0, 0, 0);
@@ -814,15 +816,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
     W st;
 
     auto team_sync = [&]() {
-        if (a.team == 1)
+        if (size() == 1)
             __syncwarp();
         else
             __syncthreads();
     };
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    while (a.whole ? seg < (long long)nb * per_base : pos < sh.r1) {
-        if (a.whole) {
+    while (whole() ? seg < (long long)nb * per_base : pos < sh.r1) {
+        if (whole()) {
             base = (int)(seg / per_base);
             sub = (int)(seg - (long long)base * per_base);
         }
@@ -834,16 +836,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
         const int real = v.count(lo, hi, a);  // 0: nothing visible, one empty group
         const int ng = max(real, 1);
         // groups [i0, i0 + take) of the segment fall to this worker
-        const int x1 = a.whole ? ng : (int)min((long long)(ng + a.lead), x0 + (sh.r1 - pos));
-        const int i0 = a.whole ? 0 : max(0, x0 - a.lead), take = a.whole ? ng : max(0, x1 - a.lead) - i0;
+        const int x1 = whole() ? ng : (int)min((long long)(ng + a.lead), x0 + (sh.r1 - pos));
+        const int i0 = whole() ? 0 : max(0, x0 - a.lead), take = whole() ? ng : max(0, x1 - a.lead) - i0;
         if (take > 0) {
-        const int nk = wt < take ? (take - wt + a.team - 1) / a.team : 0;  // this warp's groups
+        const int nk = wt < take ? (take - wt + size() - 1) / size() : 0;  // this warp's groups
 
         // bit k % 32: every row sees all of group k (of the even and the odd batches); clear past the last group
         uint32_t full0 = 0, full1 = 0;
         // descriptors of this warp's groups 32 kb .. 32 kb + 31, one for each lane
         auto batch = [&](int kb) {
-            const int k = 32 * kb + lane, i = i0 + wt + a.team * k;
+            const int k = 32 * kb + lane, i = i0 + wt + size() * k;
             Desc d{-1, 0, 0, 0};
             bool whole_group = false;
             if (k < nk && i < real) {
@@ -987,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             else
                 a.part_lse[(int64_t)part * kRows + r] = lse2;
         };
-        if (a.team == 1) {
+        if (size() == 1) {
 #pragma unroll
             for (int h = 0; h < (HALF ? 1 : 2); h++) {
                 const int r = qr + 8 * h;
@@ -1015,15 +1017,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
                 }
             }
             __syncthreads();
-            for (int k = threadIdx.x; k < rows * (D / 4); k += kThreads) {
+            for (int k = threadIdx.x; k < rows * (D / 4); k += 32 * WARPS) {
                 const int r = k / (D / 4), d = (k - r * (D / 4)) * 4;
                 float M = -INFINITY, ls = 0.f, ols = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; w++) M = fmaxf(M, s_m[w][r]);
+                for (int w = 0; w < WARPS; w++) M = fmaxf(M, s_m[w][r]);
                 const float ref = M == -INFINITY ? 0.f : M;
                 float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kWarps; w++) {
+                for (int w = 0; w < WARPS; w++) {
                     if (s_l[w][r] == 0.f) continue;
                     const float f = s_m[w][r] == -INFINITY ? 1.f : fast_exp2(s_m[w][r] - ref);
                     const float4 x = *reinterpret_cast<const float4*>(
@@ -1044,13 +1046,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             team_sync();
             if (wt == 0 && lane == 0) record_finish(a, b);
         }
-        if (!a.whole && starts && !ends) {
+        if (!whole() && starts && !ends) {
             // the worker whose share holds the segment's last group
             tail = make_int4(base, sub, last_worker(sh, pos - x0 + a.lead + ng), 0);
         }
         team_sync();  // queues and s_m are free again
         }
-        if (a.whole) {
+        if (whole()) {
             seg += a.workers;
         } else {
             pos += x1 - x0;
@@ -1061,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) gqa_stream_kernel(const 
             }
         }
     }
-    if (!a.whole && wt == 0 && lane == 0) a.tail[worker] = tail;
+    if (!whole() && wt == 0 && lane == 0) a.tail[worker] = tail;
     // after a timeout copies may still be in flight: wait for them, bounded, before the block's memory is given up
     if (!FP4 && lane == 0 && s_abort)
         for (uint32_t k = started < C::kSteps ? 0 : started - C::kSteps; k < started; k++)
@@ -1136,14 +1138,20 @@ __global__ void finish_init_kernel(int64_t* finish_ns, int64_t* t_start, int B) 
     if (threadIdx.x == 0) *t_start = (int64_t)global_timer_ns();
 }
 
-template <bool FP4, int D, bool HALF>
+template <bool FP4, int D, bool HALF, int WARPS>
 cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
-    constexpr int smem = kWarps * Lane<FP4, D>::kStages * Lane<FP4, D>::kStage + (FP4 ? 0 : 1024);
+    constexpr int smem = WARPS * Lane<FP4, D>::kStages * Lane<FP4, D>::kStage + (FP4 ? 0 : 1024);
     // once per process and device would do; the call is cheap and keeps no state
-    cudaError_t e = cudaFuncSetAttribute(gqa_stream_kernel<FP4, D, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(gqa_stream_kernel<FP4, D, HALF, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    gqa_stream_kernel<FP4, D, HALF><<<ctas, kThreads, smem, s>>>(a);
+    gqa_stream_kernel<FP4, D, HALF, WARPS><<<ctas, 32 * WARPS, smem, s>>>(a);
     return cudaGetLastError();
+}
+template <bool FP4, int D>
+cudaError_t run(const StreamArgs& a, int ctas, cudaStream_t s) {
+    const bool half = a.rows <= 8;
+    if (a.team == 2) return half ? run<FP4, D, true, 2>(a, ctas, s) : run<FP4, D, false, 2>(a, ctas, s);
+    return half ? run<FP4, D, true, 4>(a, ctas, s) : run<FP4, D, false, 4>(a, ctas, s);
 }
 
 }  // namespace
@@ -1158,8 +1166,9 @@ bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
 // team (its sum) and most where other teams share the SM -- and equal shares: the mean,
 // plus the scan of the lengths, the partials and a second kernel.  Measured: a window of
 // 128 (2 segments of about 11 groups) 8.0 us in a team of 4, 15.3 us a warp, 10.5 us in
-// shares; a window of 1021 (512 of 68) 57 us a warp, 65 us in teams, 71 us in shares; a
-// window of 4096 (512 of 258) 186 us in shares, 196 us in teams, 280 us a warp.
+// shares; a window of 1021 (512 of 68) 48.5 us in teams of 2, 57 us a warp, 65 us in teams
+// of 4, 71 us in shares; a window of 4096 (512 of 258) 184 us in teams of 2, 186 us in
+// shares, 196 us in teams of 4, 280 us a warp.
 // Shares: a team of 4 needs a fourth of the parts, a lone warp wastes nothing on short
 // segments: 48 requests of 1-14k tokens, 384 segments 47.3 us in teams, 49.6 us alone;
 // one request of 65536 tokens, 4 segments, 41 and 59 us.  lead: the same 48 requests 153,
@@ -1178,10 +1187,11 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         if (seen < tokens) tokens = seen;
     }
     const int64_t groups = (tokens / shards + kTok - 1) / kTok * span + 2 * span;
-    const int64_t ctas = (int64_t)num_sms * kCtasPerSm, warps = ctas * kWarps;
+    const int64_t warps = (int64_t)num_sms * kWarpsPerSm, ctas = warps / kWarps;
     const int64_t one = (segs + warps - 1) / warps * groups * (2 * segs <= warps ? 3 : 4) / 4 + 6;
     const int64_t four =
         (segs + ctas - 1) / ctas * ((groups + kWarps - 1) / kWarps + (2 * kWarps * segs > warps ? 14 : 8));
+    const int64_t two = (2 * segs + warps - 1) / warps * ((groups + 1) / 2 + (4 * segs > warps ? 16 : 10));
     const int64_t share = (segs * (groups + 16) + warps - 1) / warps + 30;
     p.team = 1;
     p.whole = 1;
@@ -1190,14 +1200,19 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
         best = four;
         p.team = kWarps;
     }
+    if (two < best) {
+        best = two;
+        p.team = 2;
+    }
     if (share < best) {
         p.whole = 0;
         p.team = 2 * segs >= warps ? 1 : kWarps;
     }
     p.lead = p.team == 1 ? 16 : 48;
-    const int64_t grid = p.whole ? (segs * p.team + kWarps - 1) / kWarps : ctas;
-    p.ctas = (int)(grid < ctas ? grid : ctas);
-    p.workers = p.ctas * (kWarps / p.team);
+    const int wpc = p.team == 2 ? 2 : kWarps;  // warps of a CTA
+    const int64_t grid = p.whole ? (segs * p.team + wpc - 1) / wpc : ctas;
+    p.ctas = (int)(grid < warps / wpc ? grid : warps / wpc);
+    p.workers = p.ctas * (wpc / p.team);
     p.segs = segs;
     p.off_start = 0;
     p.off_tail = 256;
@@ -1271,7 +1286,7 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const bool fp4 = c->dtype == DCP_FP4_E2M1, half = a.rows <= 8;
+    const bool fp4 = c->dtype == DCP_FP4_E2M1;
     cudaError_t e;
     if (!fp4) {
         // the pools as [page * hkv + head][64-column half][token][64 columns]; a box is 16 tokens of one head
@@ -1286,14 +1301,14 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     }
     if (c->dk == 64) {
         if (fp4)
-            e = half ? run<true, 64, true>(a, p.ctas, s) : run<true, 64, false>(a, p.ctas, s);
+            e = run<true, 64>(a, p.ctas, s);
         else
-            e = half ? run<false, 64, true>(a, p.ctas, s) : run<false, 64, false>(a, p.ctas, s);
+            e = run<false, 64>(a, p.ctas, s);
     } else {
         if (fp4)
-            e = half ? run<true, 128, true>(a, p.ctas, s) : run<true, 128, false>(a, p.ctas, s);
+            e = run<true, 128>(a, p.ctas, s);
         else
-            e = half ? run<false, 128, true>(a, p.ctas, s) : run<false, 128, false>(a, p.ctas, s);
+            e = run<false, 128>(a, p.ctas, s);
     }
     if (e != cudaSuccess || p.whole) return e;
     // few parts a segment: a row for each warp; many: a CTA for each row

@@ -44,7 +44,7 @@ struct StreamArgs {
     int32_t hq, hkv, q_len, group, rows, tiles;  // tiles of kRows query rows for each KV head
     int32_t window, sinks;
     int32_t shard_lo, shard_hi, per_shard, bt_shard0;
-    int32_t team;     // warps per team: 1 or kWarps
+    int32_t team;     // warps per team: 1, 2 (whole segments only) or 4
     int32_t workers;  // teams in the grid
     int32_t whole;    // whole segments, else equal shares
     int32_t lead;     // what a segment costs beside its groups, in groups (shares count it)

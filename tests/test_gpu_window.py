@@ -1,4 +1,6 @@
 """Decode attention under a sliding window with sinks (marked gpu) against 64 bits."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -201,3 +203,52 @@ def test_pools_past_four_gigabytes(dtype):
     dcp.dcp_kv_gather(c.desc, torch.zeros_like(pos), pos, k2)
     if dtype == "bf16":
         assert torch.equal(k2, ko)
+
+
+@pytest.mark.parametrize("d,group,q_len", [(64, 2, 1), (64, 3, 4), (128, 4, 2), (128, 16, 1)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp4"])
+@pytest.mark.parametrize("window", [130, 1000])
+def test_more_segments_than_blocks(window, dtype, d, group, q_len):
+    """400 segments on 148 SMs: whole segments, of a lone warp (short window) or of a team of two (longer)."""
+    B, hkv, page, n, i, sinks = 80, 5, 16, 2, 16, 3
+    hq, g = hkv * group, torch.Generator("cuda").manual_seed(d + group)
+    lens = torch.randint(q_len, 2200, (B,), generator=torch.Generator().manual_seed(5)).to(torch.int32)
+    lens[7] = 0
+    each = 2200 // n // page + 1
+    pages = n * B * each
+    bt = torch.randperm(pages, generator=torch.Generator().manual_seed(6)).to(torch.int32).view(n, B, each).cuda()
+    shape, dt = ((pages, hkv, page, d), torch.bfloat16) if dtype == "bf16" else \
+        ((pages, hkv, page * (d // 2 + d // 16)), torch.uint8)
+    kp, vp = (torch.empty(shape, dtype=dt, device="cuda") for _ in range(2))
+    for p in (kp, vp):  # rows that are not written: NaN
+        p.view(torch.uint8).fill_(0xFF)
+    desc = dcp.make_cache_desc(kind=dcp.DCP_GQA, dtype=dcp.DCP_BF16 if dtype == "bf16" else dcp.DCP_FP4_E2M1,
+                               n_shards=n, interleave=i, page_size=page, num_pages=pages, hq=hq, hkv=hkv, dk=d, dv=d,
+                               scale=d ** -0.5, batch=B, block_tables=bt, k_pages=kp, v_pages=vp)
+    ks, vs = [], []
+    for b, L in enumerate(lens.tolist()):
+        k, v = (torch.randn((L, hkv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+        pos = torch.arange(L, dtype=torch.int32, device="cuda")
+        req = torch.full_like(pos, b)
+        dcp.dcp_kv_append(desc, req, pos, k, v)
+        dcp.dcp_kv_gather(desc, req, pos, k, v)
+        ks.append(k), vs.append(v)
+    q = torch.randn((B, q_len, hq, d), generator=g, device="cuda").to(torch.bfloat16)
+    out, lse = torch.empty((B, q_len, hq, d), device="cuda"), torch.empty((B, q_len, hq), device="cuda")
+    size = dcp.dcp_decode_window_workspace_size(desc, B, q_len, window, sinks)
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    dcp.dcp_decode_window(desc, q, lens.cuda(), window, sinks, out, lse, ws)
+    O = torch.zeros((B, q_len, hq, d), dtype=torch.float64, device="cuda")
+    ref = torch.full((B, q_len, hq), -math.inf, dtype=torch.float64, device="cuda")
+    for b, L in enumerate(lens.tolist()):
+        for j in range(q_len):
+            at = L - q_len + j
+            p = torch.arange(max(0, at + 1), device="cuda")
+            p = p[(p < sinks) | (p > at - window)]
+            if not len(p):
+                continue
+            kd, vd = (x[b][p].double().repeat_interleave(group, 1) for x in (ks, vs))
+            s = torch.einsum("hd,phd->hp", q[b, j].double(), kd) * d ** -0.5
+            O[b, j] = torch.einsum("hp,phd->hd", s.softmax(-1), vd)
+            ref[b, j] = s.logsumexp(-1)
+    check("many segments", out, lse, O.cpu().numpy(), ref.cpu().numpy(), max(float(x.abs().max()) for x in vs if len(x)))
