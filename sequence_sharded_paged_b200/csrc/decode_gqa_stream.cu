@@ -751,8 +751,8 @@ struct Warp {
     }
 };
 
-// Two CTAs of four warps for each SM: what hides latency here is independent work
-// within a warp, which takes registers, more than a third CTA would.
+// Eight warps for each SM: what hides latency here is independent work within a warp,
+// which takes registers, more than further warps would.
 // WARPS: 4, in teams of 1 or 4, or 2, a team that takes whole segments.
 template <bool FP4, int D, bool HALF, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, kWarpsPerSm / WARPS) gqa_stream_kernel(const __grid_constant__ StreamArgs a) {
