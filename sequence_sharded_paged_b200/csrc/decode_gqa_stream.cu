@@ -234,6 +234,11 @@ struct Warp {
     // the four tokens that thread column c holds of P and V: x[t][e] is token_of(c, 2 t + e)
     __device__ __forceinline__ static int token_of(int c, int i) { return FP4 ? 4 * c + i : 2 * c + (i & 1) + 8 * (i >> 1); }
 
+    // Masked scores are -inf before they are scaled, and -inf times 0 is no weight but NaN.
+    // A scale of 0 (the caller's, or a product that 32 bits take for 0) is 2^-149 instead: it
+    // brings every finite score, below 2^128, under 2^-21, and leaves -inf what it is.
+    __device__ __forceinline__ static float row_scale(float s) { return s == 0.f ? __uint_as_float(1u) : s; }
+
     // Q fragments of rows qr (and qr + 8) of tile `tile` of KV head g
     __device__ __forceinline__ void load_q(const StreamArgs& a, int b, int g, int tile, int L, float kf) {
         const int lane = threadIdx.x & 31, qr = lane >> 2, c = lane & 3;
@@ -243,7 +248,7 @@ struct Warp {
             const bool live = r < a.rows && !(HALF && h);
             const int j = live ? r / a.group : 0, hh = live ? r - j * a.group : 0;
             at[h] = live ? L - a.q_len + j : INT_MIN / 2;
-            scale[h] = fabsf(a.scale_log2);
+            scale[h] = row_scale(fabsf(a.scale_log2));
             if (HALF && h) continue;
             const uint2* src = reinterpret_cast<const uint2*>(
                 a.q + (((int64_t)b * a.q_len + j) * a.hq + g * a.group + hh) * D);  // 4 dimensions each
@@ -272,7 +277,7 @@ struct Warp {
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 const float2 pw = row_power(amax);
                 const float f = pw.x;
-                scale[h] = fabsf(a.scale_log2) * kf * pw.y;
+                scale[h] = row_scale(fabsf(a.scale_log2) * kf * pw.y);
 #pragma unroll
                 for (int s = 0; s < KS; s++) {
                     const __half2 x = __floats2half2_rn(bf16_lo(w[s].x) * f, bf16_hi(w[s].x) * f);
