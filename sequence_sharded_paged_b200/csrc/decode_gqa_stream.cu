@@ -1077,7 +1077,9 @@ __global__ void __launch_bounds__(32 * WARPS, kWarpsPerSm / WARPS) gqa_stream_ke
 
 // Sums of the segments that are in parts: the tail of worker w and the heads of the
 // workers after it up to tail[w].z.  CTA (x, block of rows): workers x, x + gridDim.x, ..,
-// 32 at most; `wpr` warps share a row's parts.
+// 32 at most; `wpr` warps share a row's parts.  The kernel may be resident while the parts are
+// still being written (it is launched ahead), so they are read by plain loads only: the
+// read-only path is for data that does not change while a kernel lives.
 __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ StreamArgs a, int D, int wpr) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are complete and visible
     __shared__ float s_w[8];
@@ -1099,15 +1101,15 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ St
         float M = -INFINITY, ws = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live) {
-            for (int k = lane; k < K; k += 32) M = fmaxf(M, __ldg(a.part_lse + slot(k)));
+            for (int k = lane; k < K; k += 32) M = fmaxf(M, a.part_lse[slot(k)]);
 #pragma unroll
             for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
             for (int k = part; k < K; k += wpr) {
-                const float e = __ldg(a.part_lse + slot(k));
+                const float e = a.part_lse[slot(k)];
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (lane < nv) x = __ldg(reinterpret_cast<const float4*>(a.part_o + slot(k) * D) + lane);
+                if (lane < nv) x = reinterpret_cast<const float4*>(a.part_o + slot(k) * D)[lane];
                 const float w = e == -INFINITY ? 0.f : exp2f(e - ref);
                 ws += w;
                 acc.x = fmaf(w, x.x, acc.x);

@@ -67,3 +67,39 @@ def test_scales_whose_product_is_below_32_bits(hq, window):
     q = bf16(rng.standard_normal((2, 1, hq, d)) * 1e-20)
     out, lse = decode(c, to_bf16(q), window, 0)
     check("tiny scales", out, lse, *attention(c, q, window=window), max(np.abs(x).max() for x in c.v))
+
+
+# ---- requests in parts: the sum's kernel is on the SMs before the parts are written
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp4"])
+def test_parts_of_one_call_are_not_taken_for_the_next_ones(dtype):
+    """Calls back to back on one workspace, each with other queries, eagerly and in a replayed graph: every one
+    returns, bit for bit, what it returns by itself."""
+    hq, hkv, d, L = 16, 1, 128, 3500
+    rng = np.random.default_rng(12)
+    c = Cache(dtype, [rows(rng, L, hkv, d)], [rows(rng, L, hkv, d)], hq=hq, hkv=hkv, d=d, page=64, n=2, i=64)
+    qs = [to_bf16(bf16(rng.standard_normal((1, 1, hq, d)) * (1 + k))) for k in range(4)]
+    alone = [decode(c, q, 3000, 1) for q in qs]
+    for k, q in enumerate(qs):
+        check(f"alone {k}", *alone[k], *attention(c, q.double().cpu().numpy(), window=3000, sinks=1), np.abs(c.v[0]).max())
+    ws = torch.empty(dcp.dcp_decode_window_workspace_size(c.desc, 1, 1, 3000, 1), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 4096  # in parts
+    got = [(torch.empty_like(o), torch.empty_like(l)) for o, l in alone]
+
+    def calls():
+        for q, (o, l) in zip(qs, got):
+            dcp.dcp_decode_window(c.desc, q, c.seq_lens, 3000, 1, o, l, ws)
+
+    calls()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    first = [(o.clone(), l.clone()) for o, l in got]
+    with torch.cuda.graph(graph):
+        calls()
+    for o, l in got:
+        o.fill_(float("nan")), l.fill_(float("nan"))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for (o, l), (fo, fl), (ro, rl) in zip(alone, first, got):
+        assert torch.equal(fo, o) and torch.equal(fl, l) and torch.equal(ro, o) and torch.equal(rl, l)
