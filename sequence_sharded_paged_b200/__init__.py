@@ -161,6 +161,34 @@ def make_cache_desc(*, kind: int, dtype: int, n_shards: int, interleave: int, pa
                      _ptr(block_tables))
 
 
+_torch = None  # the module, once a tensor has been checked
+
+
+def _device() -> int:
+    """The current device (a tensor on a GPU is at hand: torch has initialised CUDA)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
+
+
+def _workspace(ws, device: int) -> int:
+    """Bytes of a workspace; refuse one that the kernels could not write."""
+    if ws.get_device() != device or device < 0:
+        raise ValueError(f"ws is on {ws.device}, not on the current CUDA device")
+    if not ws.is_contiguous():
+        raise ValueError(f"ws is a view with strides {ws.stride()}, not contiguous")
+    return ws.numel() * ws.element_size()
+
+
+def _decode_workspace(desc: CacheDesc, ws) -> int:
+    """Bytes of a decode call's workspace, checked where the cache is a 4-bit one."""
+    if desc.dtype == DCP_FP4_E2M1:
+        return _workspace(ws, _device())
+    return ws.numel() * ws.element_size()
+
+
 def dcp_shard_counts(seq_lens, n_shards: int, interleave: int, counts_out, stream=None) -> None:
     _check(lib().dcp_shard_counts(seq_lens.numel(), _ptr(seq_lens), n_shards, interleave, _ptr(counts_out),
                                   _stream(stream)), "dcp_shard_counts")
@@ -182,7 +210,7 @@ def dcp_decode_workspace_size(desc: CacheDesc, batch: int) -> int:
 
 def dcp_decode_partial(desc: CacheDesc, q, seq_lens, o_partial, lse, ws, stream=None) -> None:
     _check(lib().dcp_decode_partial(ctypes.byref(desc), q.shape[0], _ptr(q), _ptr(seq_lens), _ptr(o_partial),
-                                    _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                    _ptr(lse), _ptr(ws), _decode_workspace(desc, ws), _stream(stream)),
            "dcp_decode_partial")
 
 
@@ -194,7 +222,7 @@ def dcp_decode_workspace_size_ex(desc: CacheDesc, batch: int, q_len: int = 1, mo
 def dcp_decode_partial_multi(desc: CacheDesc, q, seq_lens, o_partial, lse, ws, stream=None) -> None:
     """q bf16 [B][q_len][hq][dk] -> o_partial [N][B][q_len][hq][dv], lse [N][B][q_len][hq]."""
     _check(lib().dcp_decode_partial_multi(ctypes.byref(desc), q.shape[0], q.shape[1], _ptr(q), _ptr(seq_lens),
-                                          _ptr(o_partial), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+                                          _ptr(o_partial), _ptr(lse), _ptr(ws), _decode_workspace(desc, ws),
                                           _stream(stream)), "dcp_decode_partial_multi")
 
 
@@ -204,7 +232,7 @@ def dcp_decode_merged(desc: CacheDesc, q, seq_lens, out, lse_out, ws, finish_ns=
     q's leading dimensions with dv / no trailing dimension; finish_ns int64 [B] or None."""
     q_len = 1 if q.dim() == 3 else q.shape[1]
     _check(lib().dcp_decode_merged(ctypes.byref(desc), q.shape[0], q_len, _ptr(q), _ptr(seq_lens), _ptr(out),
-                                   _ptr(lse_out), _ptr(finish_ns), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _ptr(lse_out), _ptr(finish_ns), _ptr(ws), _decode_workspace(desc, ws),
                                    _stream(stream)), "dcp_decode_merged")
 
 
@@ -217,7 +245,7 @@ def dcp_decode_rank(desc: CacheDesc, rank: int, q, seq_lens, o, lse, ws, stream=
     """Rank `rank`'s partial: q bf16 [B][hq][dk] or [B][q_len][hq][dk] -> o, lse with q's leading dims."""
     q_len = 1 if q.dim() == 3 else q.shape[1]
     _check(lib().dcp_decode_rank(ctypes.byref(desc), rank, q.shape[0], q_len, _ptr(q), _ptr(seq_lens), _ptr(o),
-                                 _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+                                 _ptr(lse), _ptr(ws), _decode_workspace(desc, ws), _stream(stream)),
            "dcp_decode_rank")
 
 
@@ -226,18 +254,6 @@ def dcp_lse_rescale(lse_all, rank: int, o, o_rs, lse_out=None, stream=None) -> N
     N, B, H = lse_all.shape
     _check(lib().dcp_lse_rescale(N, rank, B, H, o.shape[-1], _ptr(lse_all), _ptr(o), _ptr(o_rs), _ptr(lse_out),
                                  _stream(stream)), "dcp_lse_rescale")
-
-
-_torch = None  # the module, once a tensor has been checked
-
-
-def _device() -> int:
-    """The current device (a tensor on a GPU is at hand: torch has initialised CUDA)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch._C._cuda_getDevice() if _torch.cuda.is_initialized() else -1
 
 
 def _tensor(name: str, t, device: int, dtype, shape=None) -> None:
@@ -357,9 +373,10 @@ def dcp_decode_window(desc: CacheDesc, q, seq_lens, window: int, n_sinks: int, o
     _tensor("seq_lens", seq_lens, device, _torch.int32, (B,))
     _tensor("out", out, device, f32, lead + (desc.dv,))
     _tensor("lse", lse, device, f32, lead)
+    ws_bytes = _workspace(ws, device)
     _check(lib().dcp_decode_window(ctypes.byref(desc), _rank(rank), B, q_len, window, n_sinks, _ptr(q),
-                                   _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
-                                   _stream(stream)), "dcp_decode_window")
+                                   _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)),
+           "dcp_decode_window")
 
 
 # size of the library's built-in decode scratch (DCP_STATIC_SCRATCH_BYTES in dcp.h)

@@ -1,0 +1,78 @@
+"""Ends of the ranges of the operators around the decode, host side, without a GPU."""
+import pytest
+import torch
+
+import sequence_sharded_paged_b200 as dcp
+
+from test_operators_cpu import gqa
+
+
+class OnDevice:
+    """Stands for a tensor on GPU `index`, as far as the binding's checks look at one."""
+
+    def __init__(self, shape, dtype, index=0, strides=None):
+        self.host = torch.empty(shape, dtype=dtype)
+        self.shape, self.dtype, self.device, self.index = self.host.shape, dtype, f"cuda:{index}", index
+        self.strides = strides
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return self.strides is None
+
+    def stride(self):
+        return self.strides or self.host.stride()
+
+    def data_ptr(self):
+        return 1024
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.host.numel()
+
+    def element_size(self):
+        return self.host.element_size()
+
+
+def decode(name, desc, ws, q_len=1):
+    q = OnDevice((3, q_len, 16, 128), torch.bfloat16)
+    out, lse = OnDevice((3, q_len, 16, 128), torch.float32), OnDevice((3, q_len, 16), torch.float32)
+    lens = OnDevice((3,), torch.int32)
+    call = getattr(dcp, name)
+    if name == "dcp_decode_window":
+        call(desc, q, lens, 8, 0, out, lse, ws, stream=7)
+    elif name == "dcp_decode_rank":
+        call(desc, 0, q, lens, out, lse, ws, stream=7)
+    else:
+        call(desc, q, lens, out, lse, ws, stream=7)
+
+
+@pytest.mark.parametrize("ws,why", [
+    (torch.zeros(1 << 12, dtype=torch.uint8), "on cpu, not on the current CUDA device"),
+    (OnDevice((1 << 12,), torch.uint8, index=1), "on cuda:1, not on the current CUDA device"),
+    (OnDevice((1 << 12,), torch.uint8, strides=(2,)), "not contiguous"),
+    (OnDevice((1 << 12,), torch.uint8), None),
+], ids=["host", "another GPU", "strided view", "good"])
+@pytest.mark.parametrize("name", ["dcp_decode_window", "dcp_decode_merged", "dcp_decode_partial",
+                                  "dcp_decode_partial_multi", "dcp_decode_rank"])
+def test_streamed_decode_checks_its_workspace(monkeypatch, name, ws, why):
+    """The kernel writes partials through that pointer: what it could not write is refused before the call."""
+    calls = []
+
+    def entry(*args):
+        calls.append(args)
+        return dcp.DCP_OK
+
+    monkeypatch.setattr(dcp, "_device", lambda: 0)
+    monkeypatch.setattr(dcp, "_torch", torch)
+    monkeypatch.setattr(dcp, "lib", lambda: type("Library", (), {name: staticmethod(entry)}))
+    if why is None:
+        decode(name, gqa(), ws)
+        assert len(calls) == 1 and calls[0][-2] == 1 << 12
+    else:
+        with pytest.raises(ValueError, match=why):
+            decode(name, gqa(), ws)
+        assert not calls
