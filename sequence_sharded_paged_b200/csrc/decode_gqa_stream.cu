@@ -1226,9 +1226,10 @@ StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int s
     p.off_lse = p.off_o = p.off_acc = 0;
     size_t o = p.off_tail;
     using W = Warp<true, 64, false>;
-    if (c->dtype == DCP_FP4_E2M1 && rows > kRows / 2 && groups > W::kFlush) {
+    // sums in memory only where one warp can have more groups of a segment than it adds up without
+    if (c->dtype == DCP_FP4_E2M1 && rows > kRows / 2 && (groups + p.team - 1) / p.team > W::kFlush) {
         p.off_acc = o;
-        o += sizeof(float4) * kAcc * (size_t)p.ctas * kWarps;
+        o += sizeof(float4) * kAcc * (size_t)p.ctas * wpc;
         p.off_tail = o;
     }
     if (!p.whole) {

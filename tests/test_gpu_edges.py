@@ -103,3 +103,95 @@ def test_parts_of_one_call_are_not_taken_for_the_next_ones(dtype):
     torch.cuda.synchronize()
     for (o, l), (fo, fl), (ro, rl) in zip(alone, first, got):
         assert torch.equal(fo, o) and torch.equal(fl, l) and torch.equal(ro, o) and torch.equal(rl, l)
+
+
+# ---- workspace sizes
+
+def windowed_desc(B, hkv, group, d, tokens, dtype=dcp.DCP_FP4_E2M1):
+    """A descriptor for sizes only: tables of `tokens` positions on one shard."""
+    bt = torch.zeros((1, B, -(-tokens // 64)), dtype=torch.int32, device="cuda")
+    pool = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    return dcp.make_cache_desc(kind=dcp.DCP_GQA, dtype=dtype, n_shards=1, interleave=1, page_size=64, num_pages=1,
+                               hq=hkv * group, hkv=hkv, dk=d, dv=d, scale=1.0, batch=B, block_tables=bt, k_pages=pool,
+                               v_pages=pool), bt, pool
+
+
+def test_sums_in_memory_take_room_only_where_a_warp_needs_them():
+    """One segment for each pair of warps: whole segments in teams of two, no parts, so that the workspace is its
+    header and, for more groups than a warp adds up without a store, 8704 bytes for each of the 8 warps of an SM."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    size = lambda d, w: dcp.dcp_decode_window_workspace_size(d, d.batch, 1, w, 0)  # noqa: E731
+    B, hkv = sms, 4
+    desc, *keep = windowed_desc(B, hkv, 16, 128, 1 << 17)
+    assert size(desc, 300 * 16) == 256                            # 151 groups a warp
+    assert 256 < size(desc, 600 * 16) <= 256 + 8 * sms * 8704     # 301
+    few, *keep2 = windowed_desc(B, hkv, 8, 128, 1 << 17)
+    assert size(few, 600 * 16) == 256                             # 8 rows: sums stay in registers
+
+
+@pytest.mark.parametrize("B,hkv,group,q_len", [(1, 1, 1, 1), (1, 4, 16, 1), (3, 2, 16, 4), (48, 8, 8, 1), (74, 8, 16, 1),
+                                               (512, 4, 16, 1), (2, 1, 16, 64)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_4bit_workspaces_keep_to_the_stated_bound(B, hkv, group, q_len, d):
+    W = 8 * torch.cuda.get_device_properties(0).multi_processor_count
+    up = lambda x: -(-x // 256) * 256  # noqa: E731
+    parts, sums = up(16 * W) + up(128 * W) + up(128 * d * W), up(8704 * W)
+    for tokens in (64, 5000, 1 << 15, 1 << 20):
+        desc, *keep = windowed_desc(B, hkv, group, d, tokens)
+        sizes = [dcp.dcp_decode_workspace_size_ex(desc, B, q_len, m)
+                 for m in (dcp.DCP_DECODE_PARTIAL, dcp.DCP_DECODE_MERGED, dcp.DCP_DECODE_RANK)]
+        sizes += [dcp.dcp_decode_window_workspace_size(desc, B, q_len, w, 4) for w in (16, 1000, 9600, 1 << 17)]
+        assert all(256 <= s <= 256 + parts + sums for s in sizes)
+        assert sizes[0] <= dcp.DCP_STATIC_SCRATCH_BYTES
+
+
+def shared_pages(g, dtype, B, hkv, group, d, page, L):
+    """A cache of L positions on one shard whose pages all B requests read: small, whatever B."""
+    pages = -(-L // page)
+    bt = torch.arange(pages, dtype=torch.int32, device="cuda").expand(1, B, pages).contiguous()
+    shape, dt = ((pages, hkv, page, d), torch.bfloat16) if dtype == "bf16" else \
+        ((pages, hkv, page * (d // 2 + d // 16)), torch.uint8)
+    kp, vp = (torch.zeros(shape, dtype=dt, device="cuda") for _ in range(2))
+    desc = dcp.make_cache_desc(kind=dcp.DCP_GQA, dtype=dcp.DCP_BF16 if dtype == "bf16" else dcp.DCP_FP4_E2M1, n_shards=1,
+                               interleave=1, page_size=page, num_pages=pages, hq=hkv * group, hkv=hkv, dk=d, dv=d,
+                               scale=d ** -0.5, batch=B, block_tables=bt, k_pages=kp, v_pages=vp)
+    k, v = (torch.randn((L, hkv, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    v += 0.25  # a mean apart from 0: O moves on all the way
+    pos = torch.arange(L, dtype=torch.int32, device="cuda")
+    req = torch.zeros_like(pos)
+    dcp.dcp_kv_append(desc, req, pos, k, v)
+    dcp.dcp_kv_gather(desc, req, pos, k, v)
+    return desc, k, v, (bt, kp, vp)
+
+
+def attend(q, k, v, L, window, sinks):
+    """One request of attention in 64 bits on the GPU: q [q_len][hq][d], k and v [..][hkv][d]."""
+    ql, hq, d = q.shape
+    hkv = k.shape[1]
+    kd, vd = k[:L].double(), v[:L].double()
+    s = torch.einsum("jghd,pgd->jghp", q.double().view(ql, hkv, hq // hkv, d), kd) * d ** -0.5
+    p, at = torch.arange(L, device="cuda"), (L - ql + torch.arange(ql, device="cuda"))[:, None]
+    s = s.masked_fill(~((p <= at) & ((p < sinks) | (p > at - window)))[:, None, None], -float("inf"))
+    return torch.einsum("jghp,pgd->jghd", s.softmax(-1), vd).reshape(ql, hq, d), s.logsumexp(-1).reshape(ql, hq)
+
+
+def test_sums_in_memory_of_teams_of_two():
+    """The plan of the sizes above with 301 groups a warp: O goes to memory once and comes back."""
+    B, hkv, group, d, window, L = torch.cuda.get_device_properties(0).multi_processor_count, 4, 16, 128, 9600, 9733
+    g = torch.Generator("cuda").manual_seed(4)
+    desc, k, v, keep = shared_pages(g, "fp4", B, hkv, group, d, 64, L)
+    q = torch.randn((B, 1, hkv * group, d), generator=g, device="cuda").to(torch.bfloat16)
+    lens = torch.randint(9000, L + 1, (B,), generator=torch.Generator().manual_seed(4)).to(torch.int32)
+    lens[5], lens[6] = 3, L
+    out, lse = torch.empty((B, 1, hkv * group, d), device="cuda"), torch.empty((B, 1, hkv * group), device="cuda")
+    ws = torch.full((dcp.dcp_decode_window_workspace_size(desc, B, 1, window, 2),), 0xFF, dtype=torch.uint8, device="cuda")
+    guard = torch.full((ws.numel() + 4096,), 0xEE, dtype=torch.uint8, device="cuda")  # nothing is written behind the workspace
+    dcp.dcp_decode_window(desc, q, lens.cuda(), window, 2, out, lse, guard[:ws.numel()])
+    assert (guard[ws.numel():] == 0xEE).all()
+    # between two stores O is cut off 2 * 256 times, 2^-23 of at most max|V| each, the sum of the
+    # weights as often, and every weight is off by 2.1e-5 (op_ref); LSE sums 151 steps in 32 bits
+    tol_o = (2 * 512 * 2.0 ** -23 + 2 * 2.1e-5) * float(v.abs().max())
+    for b in range(B):
+        O, ref = attend(q[b], k, v, int(lens[b]), window, 2)
+        assert (out[b] - O).abs().max() <= tol_o
+        assert (lse[b] - ref).abs().max() <= 5e-5 + 151 * 2.0 ** -24
