@@ -1280,6 +1280,11 @@ cudaError_t launch_gqa_stream(const dcp_cache_desc* c, const StreamPlan& p, int 
     a.tiles = (a.rows + kRows - 1) / kRows;
     a.window = window;
     a.sinks = sinks;
+    // shard n's first position past its table, local index T, is past0 + n * interleave
+    const int64_t T = (int64_t)c->max_local_pages * c->page_size, I = c->interleave;
+    const int64_t past0 = T / I * I * c->n_shards + T % I, past = past0 + (c->n_shards - 1) * I + 1;
+    a.past0 = past0 < INT_MAX ? (int)past0 : INT_MAX;
+    a.past = past < INT_MAX ? (int)past : INT_MAX;
     a.shard_lo = shard_lo;
     a.shard_hi = shard_hi;
     a.per_shard = per_shard;

@@ -43,6 +43,7 @@ struct StreamArgs {
     int32_t n_shards, interleave, page_size, num_pages, batch, max_local_pages;
     int32_t hq, hkv, q_len, group, rows, tiles;  // tiles of kRows query rows for each KV head
     int32_t window, sinks;
+    int32_t past0, past;  // every shard has a position past its table in [past0, past), and none before past0
     int32_t shard_lo, shard_hi, per_shard, bt_shard0;
     int32_t team;     // warps per team: 1, 2 (whole segments only) or 4
     int32_t workers;  // teams in the grid
@@ -66,18 +67,20 @@ struct Counter {
 };
 
 // What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
-// when the two meet).
+// when the two meet).  Groups are counted as if all this ended at a.past: what lies past the
+// tables is still looked at, and reported, but a length that cannot be costs no more than
+// the tables' own.
 struct Visible {
     int L, first;  // length, position of query token 0 (may be negative)
     bool ends;     // sinks and window apart
     Counter cs, cl, ch;
     __device__ __forceinline__ Visible(int len, const StreamArgs& a)
-        : L(len), first(len - a.q_len), ends(false), cs(0, a), cl(0, a), ch((uint32_t)len, a) {
+        : L(len), first(len - a.q_len), ends(false), cs(0, a), cl(0, a), ch((uint32_t)min(len, a.past), a) {
         const int lo = a.window > first ? 0 : first - a.window + 1;
         if (lo > a.sinks) {
             ends = true;
-            cs = Counter((uint32_t)a.sinks, a);
-            cl = Counter((uint32_t)lo, a);
+            cs = Counter((uint32_t)min(a.sinks, a.past), a);
+            cl = Counter((uint32_t)min(lo, a.past0), a);
         }
     }
     // groups of the shard at `off`: [0, sg) and [w0, w1)

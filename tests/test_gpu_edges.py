@@ -195,3 +195,34 @@ def test_sums_in_memory_of_teams_of_two():
         O, ref = attend(q[b], k, v, int(lens[b]), window, 2)
         assert (out[b] - O).abs().max() <= tol_o
         assert (lse[b] - ref).abs().max() <= 5e-5 + 151 * 2.0 ** -24
+
+
+# ---- lengths past the block table
+
+@pytest.mark.parametrize("dtype,window,sinks", [("fp4", None, 0), ("fp4", 40, 3), ("bf16", 40, 3), ("bf16", 2 ** 31 - 1, 0),
+                                                ("fp4", 2 ** 30, 0)])
+@pytest.mark.parametrize("L", [130, 70000, 2 ** 31 - 1])
+@pytest.mark.parametrize("hq,q_len", [(4, 1), (32, 1), (4, 3)])
+def test_lengths_past_the_table_are_reported_and_cost_what_the_table_does(hq, q_len, L, dtype, window, sinks):
+    """Positions without a table entry count as absent; the work does not grow with a length that cannot be."""
+    hkv, d, have = 2, 64, 128  # four whole pages for each of two shards
+    rng = np.random.default_rng(hq)
+    c = Cache(dtype, [rows(rng, x, hkv, d) for x in (have, 33)], [rows(rng, x, hkv, d) for x in (have, 33)], hq=hq,
+              hkv=hkv, d=d, page=16, n=2, i=16)
+    q = bf16(rng.standard_normal((2, q_len, hq, d)))
+    O, LSE = attention(c, q, window=window, sinks=sinks)
+    for j in range(q_len):  # query token j of request 0 stands at L - q_len + j
+        p, at = np.arange(have), L - q_len + j
+        p = p if window is None else p[(p < sinks) | (p > at - window)]
+        p = p[p <= at]
+        for h in range(hq):
+            O[0, j, h], LSE[0, j, h] = 0, -np.inf
+            if len(p):
+                s = c.k[0][p, h // (hq // hkv)] @ q[0, j, h] * c.scale
+                w = np.exp(s - s.max())
+                O[0, j, h], LSE[0, j, h] = w @ c.v[0][p, h // (hq // hkv)] / w.sum(), s.max() + np.log(w.sum())
+    c.seq_lens[0] = L
+    out, lse = decode(c, to_bf16(q), window, sinks)
+    torch.cuda.synchronize()
+    assert dcp.dcp_get_device_status() == dcp.DCP_ERR_UNALLOCATED_PAGE
+    check("past the table", out, lse, O, LSE, max(np.abs(x).max() for x in c.v))
