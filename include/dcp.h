@@ -238,7 +238,7 @@ typedef struct {
  *  scaling    dcp_rope_scaling; factor (finite, >= 1), original (> 0), low and high
  *             (0 < low < high) are read only by the kinds that use them.
  *  attn_factor  0: 1, and for DCP_ROPE_YARN 0.1 ln(factor) + 1; otherwise the
- *             factor itself (finite, > 0).
+ *             factor itself (> 0 and finite in 32 bits).
  * Errors: DCP_ERR_INVALID_ARG, DCP_ERR_UNSUPPORTED (rot_dim).
  */
 dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double theta, int32_t scaling,

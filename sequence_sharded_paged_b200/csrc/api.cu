@@ -494,7 +494,8 @@ dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double
     const bool ends = scaling == DCP_ROPE_YARN || scaling == DCP_ROPE_SMOOTH;
     if (ends && (!(original > 0.0) || !std::isfinite(original) || !(low > 0.0) || !(high > low) || !std::isfinite(high)))
         return DCP_ERR_INVALID_ARG;
-    if (!(attn_factor >= 0.0) || !std::isfinite(attn_factor)) return DCP_ERR_INVALID_ARG;
+    const float attn = (float)attn_factor;  // kept in 32 bits, where it must not be infinite or 0 either
+    if (!(attn_factor >= 0.0) || !std::isfinite(attn) || (attn_factor > 0.0 && attn == 0.f)) return DCP_ERR_INVALID_ARG;
     if (rot_dim % 16 || rot_dim > 2 * DCP_ROPE_MAX_PAIRS) return DCP_ERR_UNSUPPORTED;
     const long double two_pi = 6.283185307179586476925286766559005768L;
     const long double d = rot_dim, f = factor;
@@ -505,7 +506,7 @@ dcp_status dcp_rope_init(dcp_rope* rope, int32_t rot_dim, int32_t layout, double
     *rope = dcp_rope{};
     rope->rot_dim = rot_dim;
     rope->layout = layout;
-    rope->attn_factor = attn_factor > 0.0 ? (float)attn_factor
+    rope->attn_factor = attn_factor > 0.0 ? attn
                         : scaling == DCP_ROPE_YARN ? (float)(0.1L * logl(f) + 1.0L) : 1.f;
     for (int i = 0; i < rot_dim / 2; i++) {
         long double w = powl(base, -2.0L * i / d);

@@ -76,3 +76,18 @@ def test_streamed_decode_checks_its_workspace(monkeypatch, name, ws, why):
         with pytest.raises(ValueError, match=why):
             decode(name, gqa(), ws)
         assert not calls
+
+
+@pytest.mark.parametrize("attn", [1e300, 3.5e38, 1e-60, 5e-324])
+def test_rope_refuses_an_attention_factor_that_32_bits_do_not_hold(attn):
+    """Stored in 32 bits it would be infinite or 0: every rotated value would be."""
+    rope = dcp.Rope()
+    with pytest.raises(dcp.DcpError) as e:
+        dcp.dcp_rope_init(rope, 64, dcp.DCP_ROPE_HALF, 1e4, attn_factor=attn)
+    assert e.value.status == dcp.DCP_ERR_INVALID_ARG
+    assert rope.rot_dim == 0  # left as it was
+
+
+@pytest.mark.parametrize("attn", [3e38, 1e-37, 1.0])
+def test_rope_keeps_an_attention_factor_that_32_bits_hold(attn):
+    assert abs(dcp.make_rope(64, attn_factor=attn).attn_factor - attn) <= attn * 2.0 ** -24
