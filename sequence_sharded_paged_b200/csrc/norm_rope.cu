@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 4) norm_rope_gqa_kernel(const __grid
         const int g = h - nq - (is_k ? 0 : nk);
         uint8_t* pool = is_k ? a.k_pages : a.v_pages;
         if (FP4)
-            store_gqa8(a, pool, tg.pg, g, tg.off, li, w.v[0], is_k ? fk : fv, mask, true);
+            store_fp4x8(a, pool, tg.pg, g, tg.off, li, w.v[0], is_k ? fk : fv, mask);
         else
             store(pool + (((int64_t)tg.pg * a.hkv + g) * a.page_size + tg.off) * (D * 2), w);
     };

@@ -144,19 +144,12 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
 }
 
 // Store 8 values (dimensions 8 li .. 8 li + 7, bf16 in `w`) of KV head g's row at
-// (pg, off) of a GQA pool.  For a 4-bit pool every lane of `both` takes part in
-// the exchange of the runs' maxima; `live` says whether this lane stores.
-__device__ __forceinline__ void store_gqa8(const AppendArgs& a, uint8_t* pool, int pg, int g, int off, int li,
-                                           const uint4& w, float factor, uint32_t both, bool live) {
+// (pg, off) of a 4-bit pool.  Every lane of `both` takes part: the row's D/8 lanes.
+__device__ __forceinline__ void store_fp4x8(const AppendArgs& a, uint8_t* pool, int pg, int g, int off, int li,
+                                            const uint4& w, float factor, uint32_t both) {
     const int D = a.dk, P = a.page_size;
-    if (a.dtype == DCP_BF16) {
-        if (live)
-            *reinterpret_cast<uint4*>(pool + ((((int64_t)pg * a.hkv + g) * P + off) * D + li * 8) * 2) = w;
-        return;
-    }
     uint8_t sb;
     const uint32_t codes = fp4_quantise8(w, factor, both, &sb);
-    if (!live) return;
     uint8_t* blk = pool + ((int64_t)pg * a.hkv + g) * fp4_block_bytes(P, D);
     *reinterpret_cast<uint32_t*>(blk + off * (D / 2) + li * 4) = codes;
     if ((li & 1) == 0) blk[P * (D / 2) + (li >> 1) * P + off] = sb;
