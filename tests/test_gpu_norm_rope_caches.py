@@ -103,3 +103,25 @@ def test_4bit_rows_are_the_appended_bf16_rows(d, rot, hq, hkv, page, n, i, norme
                 near.append(x.double().numpy())
         values = bf16(quantise4(np.array(near), factor)[2])
         assert (values == got[r]).all(-1).any(), f"run {r}: {row[r]} stored as {got[r]}"
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("normed", [False, True])
+@pytest.mark.parametrize("hq", [16, 48])
+def test_fp8_latent_rows_are_the_appended_bf16_rows(layout, normed, hq):
+    rng = np.random.default_rng(hq)
+    T, B, n, i, page, each = 203, 2, 2, 3, 64, 3
+    (plain, direct, appended), bt = caches(dcp.DCP_MLA, dcp.DCP_FP8_E4M3, hq=hq, hkv=1, d=576, dv=512, page=page, n=n, i=i,
+                                           B=B, each=each)
+    req, pos = places(rng, T, B, n, i, page, each)
+    x = rng.standard_normal((T, 576)) * np.exp(rng.standard_normal((T, 1)) * 3)
+    x[7] = 0.0
+    lat = to_bf16(x)
+    w = to_bf16(rng.standard_normal(512) * 0.3 + 1) if normed else None
+    rope = dcp.make_rope(64, layout=layout, theta=1e4)
+    for desc, *_ in (plain, direct):
+        dcp.dcp_norm_rope_append(desc, rope, req, pos, None, lat, None, None, w, 1e-6, None)
+    k = torch.empty((T, 576), dtype=torch.bfloat16, device="cuda")
+    dcp.dcp_kv_gather(plain[0], req, pos, k)
+    dcp.dcp_kv_append(appended[0], req, pos, k)
+    assert torch.equal(direct[1], appended[1]) and torch.equal(direct[3], appended[3])  # one kernel, one order
