@@ -378,15 +378,15 @@ __global__ void __launch_bounds__(kThreads) norm_rope_mla_kernel(const NormRopeA
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float scale = amax == 0.f ? 1.f : __fdiv_rn(amax, 448.f);
-    if (amax == 0.f)  // zero codes, also of the -0 that a rotation leaves
-#pragma unroll
-        for (int c = 0; c < 3; c++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) x[c][e] = 0.f;
+    const uint32_t any = amax == 0.f ? 0u : ~0u;  // zero codes in a row of zeros, also of the -0 that a rotation leaves
     uint2* dst = reinterpret_cast<uint2*>(a.k_pages + row * DK);
-    dst[lane] = fp8_quantise8(x[0], scale);
-    dst[32 + lane] = fp8_quantise8(x[1], scale);
-    if (lane < 8) dst[64 + lane] = fp8_quantise8(x[2], scale);
+    auto codes = [&](const float* v) {
+        const uint2 w = fp8_quantise8(v, scale);
+        return make_uint2(w.x & any, w.y & any);
+    };
+    dst[lane] = codes(x[0]);
+    dst[32 + lane] = codes(x[1]);
+    if (lane < 8) dst[64 + lane] = codes(x[2]);
     if (lane == 0) a.kv_scales[row] = scale;
 }
 
