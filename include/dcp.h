@@ -83,7 +83,7 @@ typedef enum { DCP_BF16 = 0, DCP_FP8_E4M3 = 1, DCP_FP4_E2M1 = 2 } dcp_dtype;
  *  dk, dv       key and value widths.  GQA: dk = dv in {64, 128}.  MLA: dk =
  *               576 (512 + 64 rope), dv = 512; the value is the first dv
  *               entries of the latent row (absorbed MLA).
- *  scale        softmax scale applied to q.k.
+ *  scale        softmax scale applied to q.k: any finite value, 0 and below it too.
  *  k_pages      GQA: keys   [num_pages][hkv][P][dk] bf16, or for fp4
  *               [num_pages][hkv] blocks of P * (dk/2 + dk/16) bytes (below).
  *               MLA: latent [num_pages][P][576] bf16, or e4m3 bytes for fp8.
@@ -311,8 +311,8 @@ size_t dcp_decode_workspace_size(const dcp_cache_desc* cache, int32_t B);
  *  DCP_ERR_WORKSPACE_TOO_SMALL  ws_bytes below dcp_decode_workspace_size();
  *  DCP_ERR_CUDA            a launch or an attribute call failed.
  * Device-side errors, read with dcp_get_device_status:
- *  DCP_ERR_UNALLOCATED_PAGE  an attended position's page is not a pool page; its
- *                          tokens are skipped;
+ *  DCP_ERR_UNALLOCATED_PAGE  an attended position's page is not a pool page, or
+ *                          lies past the block table; its tokens are skipped;
  *  DCP_ERR_TIMEOUT         a kernel gave up waiting on a copy; the outputs of that
  *                          call are then unspecified.
  */
@@ -365,7 +365,9 @@ dcp_status dcp_decode_partial_multi(const dcp_cache_desc* cache, int32_t B, int3
  * the LSE values and summed by the all-gather + reduce-scatter).  Here all
  * shards are on one GPU; the merge runs as a second kernel after the decode
  * (the kernel boundary orders the partials' stores before the merge reads
- * them, which costs less than ordering them inside the decode kernel).
+ * them, which costs less than ordering them inside the decode kernel).  Over a
+ * 4-bit cache no per-shard partial exists: the decode kernel goes through a
+ * request's shards in one pass.
  *  q_len, q, seq_lens   as dcp_decode_partial_multi (q_len = 1: one query
  *             token per request, q bf16 [B][hq][dk]).
  *  out        fp32 [B][q_len][hq][dv]: sum over shards of exp(lse_n - LSE) o_n,
@@ -379,8 +381,10 @@ dcp_status dcp_decode_partial_multi(const dcp_cache_desc* cache, int32_t B, int3
  *             For per-request latency within one batch; the values order the
  *             requests' completions, they are not a kernel timer.
  *  ws, ws_bytes  workspace of at least dcp_decode_workspace_size_ex(cache, B,
- *             q_len, DCP_DECODE_MERGED) bytes, which includes the partials (4 * N * B * q_len *
- *             hq * (dv + 1) bytes); clobbered.  Concurrent calls need distinct
+ *             q_len, DCP_DECODE_MERGED) bytes; clobbered.  It includes the partials
+ *             (4 * N * B * q_len * hq * (dv + 1) bytes), except over a 4-bit cache,
+ *             whose kernel merges the shards itself: its bound stands at
+ *             dcp_decode_partial_noalloc.  Concurrent calls need distinct
  *             workspaces.
  * Errors as dcp_decode_partial (finish_ns must be 16-byte aligned too).
  */
@@ -504,7 +508,7 @@ dcp_status dcp_lse_rescale(int32_t N, int32_t rank, int32_t B, int32_t H, int32_
  *  takes 37.9 MB and the smallest split area 39 MB; such callers use
  *  dcp_decode_partial with a workspace.
  *  A 4-bit cache has no plan of that kind and always fits: with W = 8 warps for
- *  each SM its decode takes at most
+ *  each SM its decode (every call) takes at most 256 and
  *    W * (128 * (dk+1) + 16)     the two ends of each share and their LSE
  *    W * 8704                    sums between two stores
  *  bytes, each term rounded up to 256: 30 MB on a 148-SM part.

@@ -150,9 +150,10 @@ __global__ void append_mla_fp8_kernel(AppendArgs a) {
 // GQA, 4-bit: D/16 lanes per token, a run of 16 dimensions (one scale) each.  The
 // token's page is looked up once for up to kHeadsPerLane heads, whose K and V rows are
 // all loaded before any is quantised.  The floor is HBM's, 4 D bytes in and
-// 2 (D/2 + D/16) out for each head; what bounds it is the arithmetic of the codes and
-// their scales' scattered bytes.  50021 prompt tokens of 8 heads of 128, 263 MB: append
-// 60 us, 4.4 TB/s (68 us with a byte stored for each scale); read-back 43 us, 6.1 TB/s.
+// 2 (D/2 + D/16) out for each head; what bounds it is the arithmetic of the codes (issue
+// slots and the ALU pipe are 74% busy, DRAM 48%).  50021 prompt tokens of 8 heads of 128,
+// 263 MB: append 59 us, 4.5 TB/s (68 us with a byte stored for each scale, whose scattered
+// stores were waited for); read-back 44 us, 5.9 TB/s.
 constexpr int kHeadsPerLane = 2;
 
 // A warp holds the same head's rows of four tokens that follow one another in the call:

@@ -28,9 +28,12 @@
 // with K a group ahead: 220 us instead of 195 us.)  Q K^T is exact products, P has
 // three bf16 terms (24 bits), and O is summed by additions that round.
 //
-// 4-bit caches.  Bound by the arithmetic: codes to fp16, times their scale, and 16 + 32
-// matrix instructions (16 + 16 up to 8 rows) a group, which take at least 192 us of
-// the 299 us below.  The dimensions of a k-step and the tokens of a group may be
+// 4-bit caches.  Bound by the latency of the arithmetic: codes to fp16, times their scale,
+// and 16 + 32 + 2 matrix instructions (16 + 16 + 1 up to 8 rows) a group.  A loop of such
+// instructions alone takes a scheduler 10.75 cycles each, 192 us for the first case below;
+// but with two warps a scheduler, all that the registers allow, neither the tensor pipe
+// (42% busy) nor the issue slots (43%) are full, and waits of a fixed length come first among
+// the stalls.  The dimensions of a k-step and the tokens of a group may be
 // permuted freely (Q, and P from S, are permuted alike), so each thread takes 16 or 8
 // CONSECUTIVE bytes of a row as its operands:
 //   Q K^T  thread (n = lane / 4, c = lane % 4), token tile t: token
@@ -53,11 +56,11 @@
 //
 // Measured, K and V bytes / time, of a copy's 6.56 TB/s:
 //   bf16   128 requests, 64 / 4 heads of 128, window 4096: 1081 MB, 184 us, 5.9 TB/s, 90%
-//          1 request, window 65536: 134 MB, 41 us (20 us of it streaming, 9 us until the
+//          1 request, window 65536: 134 MB, 39 us (20 us of it streaming, 9 us until the
 //          first bytes, the rest the sums of 300 parts and two launches)
 //          1 request, window 128, 8 / 2 heads of 64: 8 us, latency
-//   4-bit  24 requests of 32k-128k, 64 / 4 heads: 906 MB, 299 us, 3.0 TB/s (the instructions)
-//          48 requests of 1-14k, 64 / 8 heads: 85 MB, 47 us (8 rows; half of the segments
+//   4-bit  24 requests of 32k-128k, 64 / 4 heads: 906 MB, 297 us, 3.0 TB/s
+//          48 requests of 1-14k, 64 / 8 heads: 85 MB, 46 us (8 rows; half of the segments
 //          are of 5 groups and cost as much as 48)
 //          64 requests, 4 tokens each, window 1021: 68 MB, 48.5 us (512 segments, two warps each)
 //          2 requests of 400, 8 / 2 heads of 64: 8 us, latency
@@ -1178,9 +1181,11 @@ bool gqa_stream_supported(int hq, int hkv, int dk, int q_len) {
 // shares, 196 us in teams of 4, 280 us a warp.
 // Shares: a team of 4 needs a fourth of the parts, a lone warp wastes nothing on short
 // segments: 48 requests of 1-14k tokens, 384 segments 47.3 us in teams, 49.6 us alone;
-// one request of 65536 tokens, 4 segments, 41 and 59 us.  lead: the same 48 requests 153,
-// 65, 49 and 47 us at 4, 16, 32 and 48 groups a segment (teams), 72, 53, 50 and 52 us at
-// 4, 8, 16 and 32 (a warp).
+// one request of 65536 tokens, 4 segments, 41 and 59 us (39 us since the sums of parts are
+// read by plain loads).  The longest segment is taken from the tables' width, which a server
+// keeps wider than its requests are long: the choice is then that of long requests.  lead: the same 48 requests 153,
+// 65, 49 and 47 us at 4, 16, 32 and 48 groups a segment (teams; above 48 not measured), 72,
+// 53, 50 and 52 us at 4, 8, 16 and 32 (a warp).
 StreamPlan gqa_stream_plan(const dcp_cache_desc* c, int q_len, int window, int sinks, int shards, bool per_shard,
                            int num_sms) {
     StreamPlan p;
