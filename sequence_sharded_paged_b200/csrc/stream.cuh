@@ -69,7 +69,8 @@ struct Counter {
 // What request b's query tokens can see: positions [0, sinks) and [lo, L) (sinks = 0
 // when the two meet).  Groups are counted as if all this ended at a.past: what lies past the
 // tables is still looked at, and reported, but a length that cannot be costs no more than
-// the tables' own.
+// the tables' own.  (Up to a.past a window may lie behind what is missing, and is counted as
+// it is.)
 struct Visible {
     int L, first;  // length, position of query token 0 (may be negative)
     bool ends;     // sinks and window apart
@@ -80,7 +81,7 @@ struct Visible {
         if (lo > a.sinks) {
             ends = true;
             cs = Counter((uint32_t)min(a.sinks, a.past), a);
-            cl = Counter((uint32_t)min(lo, a.past0), a);
+            cl = Counter((uint32_t)(len > a.past ? min(lo, a.past0) : lo), a);
         }
     }
     // groups of the shard at `off`: [0, sg) and [w0, w1)

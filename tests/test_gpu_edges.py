@@ -226,3 +226,25 @@ def test_lengths_past_the_table_are_reported_and_cost_what_the_table_does(hq, q_
     torch.cuda.synchronize()
     assert dcp.dcp_get_device_status() == dcp.DCP_ERR_UNALLOCATED_PAGE
     check("past the table", out, lse, O, LSE, max(np.abs(x).max() for x in c.v))
+
+
+@pytest.mark.parametrize("dtype", ["fp4", "bf16"])
+@pytest.mark.parametrize("q_len", [1, 2])
+def test_a_window_past_a_page_that_is_not_there_reports_nothing(dtype, q_len):
+    """Tables that end inside a run of positions: position 124 has no entry, but it lies behind the window."""
+    hq, hkv, d, L, window = 4, 2, 64, 129, 3
+    rng = np.random.default_rng(21)
+    c = Cache(dtype, [rows(rng, x, hkv, d) for x in (L, 20)], [rows(rng, x, hkv, d) for x in (L, 20)], hq=hq, hkv=hkv, d=d,
+              page=16, n=2, i=5)
+    assert c.bt.shape[2] == 5      # shard 0 owns 65 of the 129 positions, the last of them 124
+    c.bt = c.bt[:, :, :4].contiguous()
+    c.desc = c.make_desc()
+    q = bf16(rng.standard_normal((2, q_len, hq, d)))
+    out, lse = decode(c, to_bf16(q), window, 0)
+    check("behind the window", out, lse, *attention(c, q, window=window), max(np.abs(x).max() for x in c.v))
+    torch.cuda.synchronize()
+    assert dcp.dcp_get_device_status() == dcp.DCP_OK
+    c.seq_lens[0] = 131            # 129, 130, .. : shard 1's 65th and shard 0's 66th are past the tables
+    decode(c, to_bf16(q), window, 0)
+    torch.cuda.synchronize()
+    assert dcp.dcp_get_device_status() == dcp.DCP_ERR_UNALLOCATED_PAGE
